@@ -425,6 +425,57 @@ elmo_status elmo_precision_at_k(const int32_t* idx_dev, int32_t B, int32_t k, co
 #define ELMO_WAIT_CHECK_SITE 99
 elmo_status elmo_check_bounded_wait(int64_t limit_cycles, int32_t* status_dev, void* stream);
 
+/*
+ * elmo_q4_pack -- a copy of a head's weights in 4 bits.
+ *
+ * Passage: the head dominates the model's memory (abstract); the paper trains
+ * it in 16 or 8 bits.  This copy is for answering a few queries, where the
+ * time is that of reading the head.  Every `group` consecutive weights of a
+ * label share the scale s = bf16(max|w| / 7) (the quotient in fp32, both
+ * roundings to nearest even); a weight's code is
+ * u = clamp(rne(w / s), -8, 7) + 8 and stands for s (u - 8).  A group of
+ * zeros, or one whose scale underflows, has s = 0 and codes 8; a group holding
+ * a NaN or an infinity has s = NaN and codes 8.
+ *
+ *   W_dev      : [L x d] weights, bf16 bits or E4M3 / E5M2 codes by dt, as in
+ *                elmo_init_head (ELMO_FP8_E4M3_GE5M2 reads as ELMO_FP8_E4M3).
+ *   L, d       : 1 <= L < ELMO_MAX_LABELS; d a multiple of 64 in [64, 4096].
+ *   group      : 32, 64 or 128, dividing d.
+ *   codes_dev  : uint8 [L x d/2], written: byte i of a row holds elements 2i
+ *                (low nibble) and 2i + 1 (high nibble).
+ *   scales_dev : bf16 [L x d/group], written.
+ */
+elmo_status elmo_q4_pack(const void* W_dev, int64_t L, int32_t d, elmo_dtype dt, int32_t group, void* codes_dev,
+                         void* scales_dev, void* stream);
+
+/*
+ * elmo_q4_unpack -- the bf16 weights that a 4-bit copy stands for:
+ * W = bf16(s (u - 8)), one rounding to nearest even.  They can be wrapped as a
+ * head (elmo_init_head with ELMO_BF16).
+ *   codes_dev, scales_dev, L, d, group : as written by elmo_q4_pack.
+ *   W_dev : bf16 [L x d], written.
+ */
+elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_t L, int32_t d, int32_t group,
+                           void* W_dev, void* stream);
+
+/*
+ * elmo_q4_scores -- the scores of a few queries against a 4-bit copy:
+ *   Z[b, l] = sum_g s[l, g] sum_{j in group g} x[b, j] (u[l, j] - 8),
+ * each group's sum and the sum over the groups in fp32.  The queries enter
+ * with their bf16 values scaled by a power of two each (undone in fp32);
+ * values below 2^-32 of their query's largest magnitude are rounded, to within
+ * 2^-40 of that magnitude.  Any 4-bit copy in the stated layout may be given.
+ *
+ *   codes_dev, scales_dev, L, d, group : as in elmo_q4_pack.
+ *   X_dev : bf16 [B x d], 1 <= B <= ELMO_MAX_PREDICT_BATCH.  Batches are taken
+ *           32 queries (fewer for d above 1024) to a pass over the codes.
+ *   Z_dev : fp32, row b at Z_dev + b * ldz, ldz >= L; entries [L, ldz) of a
+ *           row are left as they are.
+ * A wait that ran out leaves NaN in the scores it could not form.
+ */
+elmo_status elmo_q4_scores(const void* codes_dev, const void* scales_dev, int64_t L, int32_t d, int32_t group,
+                           const void* X_dev, int32_t B, float* Z_dev, int64_t ldz, void* stream);
+
 /* Message of the most recent failure on the calling thread ("" if none). */
 const char* elmo_last_error(void);
 

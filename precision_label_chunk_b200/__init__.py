@@ -11,6 +11,7 @@ The names match the C entry points:
   elmo_train_step_chunked, elmo_train_step_noalloc, elmo_forward_chunk,
   elmo_topk_predict, elmo_topk_merge, elmo_sr_round, elmo_sr_draws,
   elmo_precision_at_k, elmo_kahan_sgd, elmo_round_bf16,
+  elmo_q4_pack, elmo_q4_unpack, elmo_q4_scores,
   elmo_check_bounded_wait, elmo_sync_status,
   elmo_head_workspace_bytes and the tracing calls.
 """
@@ -31,6 +32,7 @@ __all__ = [
     "elmo_profile_read", "elmo_launch_count", "KERNEL_CLASSES", "elmo_train_step_noalloc",
     "elmo_check_bounded_wait", "WAIT_CHECK_SITE", "elmo_precision_at_k", "elmo_init_head_shard",
     "elmo_topk_merge", "MAX_SHARDS", "MAX_TOTAL_LABELS", "elmo_kahan_sgd", "elmo_round_bf16", "elmo_last_error",
+    "elmo_q4_pack", "elmo_q4_unpack", "elmo_q4_scores",
 ]
 
 BF16 = 0
@@ -106,6 +108,9 @@ def _declare(L):
     L.elmo_launch_count.argtypes = [P, ctypes.POINTER(i64)]
     L.elmo_check_bounded_wait.argtypes = [i64, P, P]
     L.elmo_precision_at_k.argtypes = [P, i32, i32, P, P, i32, P, P]
+    L.elmo_q4_pack.argtypes = [P, i64, i32, ctypes.c_int, i32, P, P, P]
+    L.elmo_q4_unpack.argtypes = [P, P, i64, i32, i32, P, P]
+    L.elmo_q4_scores.argtypes = [P, P, i64, i32, i32, P, i32, P, i64, P]
     for name in ("elmo_profile_enable", "elmo_profile_reset", "elmo_profile_read", "elmo_launch_count","elmo_init_head", "elmo_head_destroy", "elmo_train_step_chunked", "elmo_forward_chunk",
                  "elmo_topk_predict", "elmo_sr_round", "elmo_sr_draws", "elmo_sync_status",
                  "elmo_head_workspace_bytes", "elmo_topk_uncertified_rows", "elmo_topk_screen_scores"):
@@ -140,6 +145,35 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _here(*tensors):
+    """Checks that the tensors live on the current device, whose stream the call uses."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _shape(name, t, shape, *dtypes):
+    """Checks a tensor's shape and element type (its layout where the call takes it dense is _ptr's)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+
+
+def _rows_ptr(name, t):
+    """(pointer, row pitch in elements) of a 2-D tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if pitch < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap")
+    return ctypes.c_void_p(t.data_ptr()), pitch
 
 
 def _dt(dtype) -> int:
@@ -313,6 +347,53 @@ def elmo_precision_at_k(idx: torch.Tensor, rowptr: torch.Tensor, cols: torch.Ten
     B, k = idx.shape
     _check(load().elmo_precision_at_k(_ptr(idx), B, k, _ptr(rowptr), _ptr(cols), cols.numel(), _ptr(p),
                                       _stream(stream)))
+
+
+_BF16_BITS = (torch.bfloat16, torch.int16)
+_FP8_CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _q4_copy(codes, scales):
+    """(L, d, group) of a 4-bit copy."""
+    if codes.dim() != 2 or scales.dim() != 2 or scales.shape[1] < 1:
+        raise ValueError("codes must be [L, d / 2] and scales [L, d / group]")
+    L, d = codes.shape[0], 2 * codes.shape[1]
+    _shape("codes", codes, (L, d // 2), torch.uint8)
+    _shape("scales", scales, (L, scales.shape[1]), *_BF16_BITS)
+    if d % scales.shape[1]:
+        raise ValueError(f"{scales.shape[1]} scales a row do not divide d = {d}")
+    return L, d, d // scales.shape[1]
+
+
+def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """The 4-bit copy of a head's weights W [L, d] (bf16, E4M3 or E5M2 by dtype): codes uint8 [L, d / 2], two a
+    byte with the even element low, and scales bf16 [L, d / group]; see include/elmo.h."""
+    dt = _dt(dtype)
+    L, d = W.shape
+    _shape("W", W, (L, d), *(_BF16_BITS if dt == BF16 else _FP8_CODES))
+    _shape("codes", codes, (L, d // 2), torch.uint8)
+    _shape("scales", scales, (L, d // int(group) if group > 0 else 0), *_BF16_BITS)
+    _here(W, codes, scales)
+    _check(load().elmo_q4_pack(_ptr(W), L, d, dt, int(group), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def elmo_q4_unpack(codes: torch.Tensor, scales: torch.Tensor, W: torch.Tensor, stream=None):
+    """W (bf16 [L, d]) = the weights that a 4-bit copy stands for."""
+    L, d, group = _q4_copy(codes, scales)
+    _shape("W", W, (L, d), *_BF16_BITS)
+    _here(W, codes, scales)
+    _check(load().elmo_q4_unpack(_ptr(codes), _ptr(scales), L, d, group, _ptr(W), _stream(stream)))
+
+
+def elmo_q4_scores(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, Z: torch.Tensor, stream=None):
+    """Z (fp32 [B, L], rows may have a pitch) = the scores of the queries X (bf16 [B, d]) against a 4-bit copy."""
+    L, d, group = _q4_copy(codes, scales)
+    B = X.shape[0]
+    _shape("X", X, (B, d), *_BF16_BITS)
+    _shape("Z", Z, (B, L), torch.float32)
+    _here(codes, scales, X, Z)
+    z, ldz = _rows_ptr("Z", Z)
+    _check(load().elmo_q4_scores(_ptr(codes), _ptr(scales), L, d, group, _ptr(X), B, z, ldz, _stream(stream)))
 
 
 def elmo_check_bounded_wait(limit_cycles: int, status: torch.Tensor, stream=None):

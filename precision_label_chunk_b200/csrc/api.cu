@@ -14,6 +14,7 @@
 
 #include "../../include/elmo.h"
 #include "elmo_internal.h"
+#include "elmo_operators.h"
 
 namespace {
 
@@ -125,6 +126,17 @@ elmo_status check_labels_args(const elmo_head* h, const void* X, int32_t B, cons
   if (nnz > ELMO_MAX_NNZ) return fail(ELMO_EUNSUPPORTED, "nnz = %d above %d", nnz, ELMO_MAX_NNZ);
   if (!aligned16(X)) return fail(ELMO_EINVAL, "X is not 16-byte aligned");
   (void)h;
+  return ELMO_OK;
+}
+
+// The shape of a 4-bit copy of a head (elmo_q4_*).
+elmo_status check_q4(const void* codes, const void* scales, int64_t L, int32_t d, int32_t group) {
+  if (!codes || !scales) return fail(ELMO_EINVAL, "null codes or scales");
+  if (L < 1 || L >= ELMO_MAX_LABELS) return fail(ELMO_EINVAL, "L = %lld outside [1, 2^24)", (long long)L);
+  if (d < 64 || d > 4096 || d % 64 != 0) return fail(ELMO_EINVAL, "d = %d: need a multiple of 64 in [64, 4096]", d);
+  if (group != 32 && group != 64 && group != 128) return fail(ELMO_EINVAL, "group = %d: need 32, 64 or 128", group);
+  if (d % group != 0) return fail(ELMO_EINVAL, "d = %d is not a multiple of group = %d", d, group);
+  if (!aligned16(codes) || !aligned16(scales)) return fail(ELMO_EINVAL, "codes or scales not 16-byte aligned");
   return ELMO_OK;
 }
 
@@ -544,6 +556,50 @@ elmo_status elmo_topk_merge(const int32_t* idx_dev, const float* score_dev, int3
   if (k < 1 || k > ELMO_MAX_TOPK) return fail(ELMO_EINVAL, "k = %d outside [1, %d]", k, ELMO_MAX_TOPK);
   ELMO_CUDA(elmo::launch_topk_merge(idx_dev, score_dev, P, B, k, idx_out_dev, score_out_dev, as_stream(stream)),
             "topk merge");
+  return ELMO_OK;
+}
+
+elmo_status elmo_q4_pack(const void* W_dev, int64_t L, int32_t d, elmo_dtype dt, int32_t group, void* codes_dev,
+                         void* scales_dev, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  elmo_status st = check_q4(codes_dev, scales_dev, L, d, group);
+  if (st != ELMO_OK) return st;
+  if (!W_dev || !aligned16(W_dev)) return fail(ELMO_EINVAL, "W null or not 16-byte aligned");
+  if (dt != ELMO_BF16 && dt != ELMO_FP8_E4M3 && dt != ELMO_FP8_E4M3_GE5M2 && dt != ELMO_FP8_E5M2)
+    return fail(ELMO_EINVAL, "unknown dtype %d", (int)dt);
+  const int fmt = dt == ELMO_FP8_E4M3_GE5M2 ? (int)ELMO_FP8_E4M3 : (int)dt;
+  ELMO_CUDA(elmo::launch_q4_pack(W_dev, L, d, fmt, group, static_cast<uint8_t*>(codes_dev),
+                                 static_cast<uint16_t*>(scales_dev), as_stream(stream)), "q4_pack");
+  return ELMO_OK;
+}
+
+elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_t L, int32_t d, int32_t group,
+                           void* W_dev, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  elmo_status st = check_q4(codes_dev, scales_dev, L, d, group);
+  if (st != ELMO_OK) return st;
+  if (!W_dev || !aligned16(W_dev)) return fail(ELMO_EINVAL, "W null or not 16-byte aligned");
+  ELMO_CUDA(elmo::launch_q4_unpack(static_cast<const uint8_t*>(codes_dev), static_cast<const uint16_t*>(scales_dev), L,
+                                   d, group, static_cast<uint16_t*>(W_dev), as_stream(stream)), "q4_unpack");
+  return ELMO_OK;
+}
+
+elmo_status elmo_q4_scores(const void* codes_dev, const void* scales_dev, int64_t L, int32_t d, int32_t group,
+                           const void* X_dev, int32_t B, float* Z_dev, int64_t ldz, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  elmo_status st = check_q4(codes_dev, scales_dev, L, d, group);
+  if (st != ELMO_OK) return st;
+  if (!X_dev || !Z_dev) return fail(ELMO_EINVAL, "null X or Z");
+  if (!aligned16(X_dev)) return fail(ELMO_EINVAL, "X is not 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(Z_dev) & 3u) return fail(ELMO_EINVAL, "Z is not 4-byte aligned");
+  if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
+  if (ldz < L) return fail(ELMO_EINVAL, "ldz = %lld below L = %lld", (long long)ldz, (long long)L);
+  ELMO_CUDA(elmo::launch_q4_scores(static_cast<const uint8_t*>(codes_dev), static_cast<const uint16_t*>(scales_dev), L,
+                                   d, group, static_cast<const uint16_t*>(X_dev), B, Z_dev, ldz, as_stream(stream)),
+            "q4_scores");
   return ELMO_OK;
 }
 

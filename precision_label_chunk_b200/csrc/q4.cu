@@ -1,0 +1,536 @@
+// q4.cu -- a head held in 4 bits: codes with a scale for every group of
+// consecutive weights of a label, made from the head's weights, read back, and
+// multiplied with a few queries.
+//
+// The classifier head dominates the model's memory ("ELMO: Efficiency via
+// Low-precision and Peak Memory Optimization in Large Output Spaces",
+// abstract); a query reads all of it, so the time of serving a few queries is
+// that of reading the head, and a quarter of the bytes is a quarter of it.
+//
+// Format.  A group of G (32, 64 or 128) weights of one label has the bf16
+// scale s = bf16(max|w| / 7) and codes u = rne(w / s) + 8, so that w stands
+// for s (u - 8); two codes a byte, the even element in the low nibble.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "elmo_common.cuh"
+#include "elmo_internal.h"
+#include "elmo_operators.h"
+#include "tc_ptx.cuh"
+
+namespace elmo {
+namespace {
+
+using namespace tc;
+
+// ---------------------------------------------------------------- pack, unpack
+// Rows are whole groups, so the matrix is one run of groups: a thread takes 16
+// consecutive weights, the G / 16 threads of a group share their maximum.
+//
+// w / s is rounded to the nearest whole number without a division: with
+// r = 1 / s to within a few units in the last place, t = w r is near w / s,
+// and w / s is either exactly k + 1/2 or at least 2^-9 away from it (w and s
+// have 8-bit significands a 2^e and b 2^f; near k + 1/2 >= 1/2 they have
+// e >= f - 1, so w / s - (k + 1/2) is a multiple of 1 / (2 b)).  Rounding t to
+// a multiple of 2^-13 (the sum with 1.5 2^10) therefore restores exact ties
+// and moves nothing else across one, and the sum with 1.5 2^23 then rounds
+// ties to even.  Scales below 2^-100, whose reciprocal may overflow and whose
+// own rounding may be coarse, take the division.
+//
+// HBM-bound: bytes of W, half a byte a weight, the scales.  Five fp32
+// operations a weight keep the arithmetic below the time of the bytes.
+constexpr int kPackThreads = 256;
+
+template <int kFormat>
+__device__ __forceinline__ void load16(const void* W, int64_t i, float (&w)[16]) {
+  if (kFormat == ELMO_BF16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + i);
+    const uint4 a = __ldcs(p), b = __ldcs(p + 1);
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[2 * e] = __uint_as_float(v[e] << 16);
+      w[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+    }
+  } else {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(W) + i));
+    const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float f[4];
+      if (kFormat == ELMO_FP8_E5M2) e5m2x4_to_f32(v[e], f);
+      else e4m3x4_to_f32(v[e], f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[4 * e + q] = f[q];
+    }
+  }
+}
+
+template <int kFormat>
+__global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const void* __restrict__ W, int64_t n16, int lanes,
+                                                               uint2* __restrict__ codes,
+                                                               uint16_t* __restrict__ scales) {
+  // every thread of a warp stays for the shuffles; groups never straddle warps
+  const int64_t stride = (int64_t)gridDim.x * kPackThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kPackThreads; i0 < n16; i0 += stride) {
+    const int64_t i = i0 + threadIdx.x;
+    float w[16];
+    uint32_t m = 0;                                    // the magnitudes' bits order them, NaN above inf
+    if (i < n16) {
+      load16<kFormat>(W, i * 16, w);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(w[e]) & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = 0.0f;
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const bool finite = m < 0x7F800000u;
+    const uint16_t sb = finite ? f32_to_bf16_rn(__fdiv_rn(__uint_as_float(m), 7.0f)) : (uint16_t)0x7FC0u;
+    const float s = bf16_to_f32(sb);
+    uint32_t q[2] = {0u, 0u};
+    if (s >= 0x1p-100f) {
+      const float r = __frcp_rn(s);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float t = __fmul_rn(w[e], r);
+        t = __fsub_rn(__fadd_rn(t, 1536.0f), 1536.0f);
+        // |t| <= 7 (1 + 2^-8): the low four bits of the sum's integer are the code
+        q[e >> 3] |= (__float_as_uint(__fadd_rn(t, 12582920.0f)) & 15u) << (4 * (e & 7));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float t = s > 0.0f ? rintf(__fdiv_rn(w[e], s)) : 0.0f;   // NaN and zero scales: code 8
+        t = fminf(fmaxf(t, -8.0f), 7.0f);
+        q[e >> 3] |= (uint32_t)((int)t + 8) << (4 * (e & 7));
+      }
+    }
+    if (i < n16) {
+      codes[i] = make_uint2(q[0], q[1]);
+      if ((threadIdx.x & (lanes - 1)) == 0) scales[i / lanes] = sb;
+    }
+  }
+}
+
+// Eight codes -> eight values (u - 8) s in bf16, each rounded once: 0x4300 | u
+// is the bf16 number 128 + u, 136 is subtracted exactly, and the product with
+// the scale rounds.
+__device__ __forceinline__ uint4 q4_values8(uint32_t c, __nv_bfloat162 s2) {
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t b = c >> (8 * e);
+    const uint32_t v = 0x43004300u | (b & 0xFu) | ((b & 0xF0u) << 12);
+    const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
+    const __nv_bfloat162 w = __hmul2(q, s2);
+    o[e] = *reinterpret_cast<const uint32_t*>(&w);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__global__ void __launch_bounds__(kPackThreads) q4_unpack_kernel(const uint2* __restrict__ codes,
+                                                                 const uint16_t* __restrict__ scales, int64_t n16,
+                                                                 int lanes, uint4* __restrict__ W) {
+  const int64_t stride = (int64_t)gridDim.x * kPackThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < n16; i += stride) {
+    const uint2 c = __ldcs(codes + i);
+    const __nv_bfloat16 s = __ushort_as_bfloat16(scales[i / lanes]);
+    const __nv_bfloat162 s2 = __halves2bfloat162(s, s);
+    __stcs(W + 2 * i, q4_values8(c.x, s2));
+    __stcs(W + 2 * i + 1, q4_values8(c.y, s2));
+  }
+}
+
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  return n;
+}
+
+int flat_grid(int64_t threads) {
+  const int64_t want = (threads + kPackThreads - 1) / kPackThreads, most = (int64_t)device_sms() * 16;
+  return (int)(want < most ? want : most);
+}
+
+// ---------------------------------------------------------------- scores
+// Z[b, l] = sum_g s[l, g] sum_{j in g} x[b, j] (u[l, j] - 8).
+//
+// Warp w of a CTA owns 16 kMT labels of a tile as the M rows of m16n8k16
+// matrix instructions (fp16 operands, fp32 sums), queries are the N columns.
+// These instructions take A from registers, where the codes are unpacked; the
+// tcgen05 ones would need them written back to shared memory at four times
+// the bytes, and with at most a few dozen columns the tensor pipe is idle
+// either way.
+//
+// Codes: a TMA ring of 128-byte boxes (256 codes of every label of the tile,
+// 128-byte swizzle).  Thread (g, t) of a warp (g = lane / 4, t = lane % 4)
+// holds, for its rows, the G / 4 consecutive codes t of each group: the K
+// order inside a group is free as long as X follows it, and all K slots of an
+// instruction lie in one group, so the group's sum comes out on its own in
+// fp32 and is scaled in fp32.  The row of a tile that a fragment row stands
+// for is chosen so that the shared loads have no bank conflicts.
+//
+// Codes to fp16 numbers: a nibble in bits 0-3 with 0x6400 is 1024 + u, in bits
+// 4-7 it is 1024 + 16 u; one subtraction, or one multiply-add with 1/16, gives
+// u - 8 exactly.  Nine instructions for eight codes.
+//
+// X: fp16 in fragment order, each query scaled by the power of two that puts
+// its largest magnitude into [2^14, 2^15).  A bf16 number's 8 bits fit fp16's
+// 11; numbers below 2^-32 of the query's largest are rounded, to within 2^-40
+// of it, which is far below the fp32 sums' own rounding.
+constexpr int kQKB = 128;                 // bytes of a box's row: 256 codes
+constexpr int kQMaxStages = 8;
+constexpr long long kQWait = 4000000000LL;
+constexpr size_t kQSmem = 225 * 1024;     // of the 227 KB a CTA may have
+constexpr int kQMaxNB = 4;                // 8-query column blocks of one pass
+
+template <int kG> __device__ __forceinline__ int q4_row(int g) {
+  // 16-byte loads go by quarter warps (rows g, g + 1), 8-byte loads by half warps (4 rows)
+  if (kG == 128) return ((g & 1) << 2) | (g >> 1);
+  if (kG == 64) return ((g & 3) << 1) | (g >> 2);
+  return g;
+}
+
+template <int kWords> __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&v)[kWords]);
+template <> __device__ __forceinline__ void lds_words<1>(uint32_t addr, uint32_t (&v)[1]) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
+}
+template <> __device__ __forceinline__ void lds_words<2>(uint32_t addr, uint32_t (&v)[2]) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
+}
+template <> __device__ __forceinline__ void lds_words<4>(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
+// 8 codes (elements 0..7, nibble i = element i) -> pairs (0,4), (1,5), (2,6), (3,7) of u - 8
+__device__ __forceinline__ void q4_pairs(uint32_t c, uint32_t (&p)[4]) {
+  const uint32_t hi = c >> 8;
+  const __half2 m1032 = __half2half2(__ushort_as_half(0x6408));          // 1032
+  const __half2 r16 = __half2half2(__ushort_as_half(0x2C00));            // 1 / 16
+  const __half2 m72 = __half2half2(__ushort_as_half(0xD480));            // -72
+  uint32_t w[4] = {(c & 0x000F000Fu) | 0x64006400u, (c & 0x00F000F0u) | 0x64006400u,
+                   (hi & 0x000F000Fu) | 0x64006400u, (hi & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 v = *reinterpret_cast<const __half2*>(&w[e]);
+    const __half2 q = (e & 1) ? __hfma2(v, r16, m72) : __hsub2(v, m1032);
+    p[e] = *reinterpret_cast<const uint32_t*>(&q);
+  }
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+struct SmemQ {
+  uint64_t full[kQMaxStages], empty[kQMaxStages];
+  int32_t exponent[8 * kQMaxNB];
+  int abort;
+};
+
+struct Q4Args {
+  const uint16_t* scales;
+  const uint16_t* X;
+  float* Z;
+  int64_t L, ldz;
+  int32_t d, B, stages;
+};
+
+// kMT: 16-label blocks of a warp; kNB: 8-query blocks of this pass (grid.y
+// walks over the batch 8 kNB queries at a time); kWarps warps of labels and
+// one for the TMA.
+template <int kG, int kMT, int kNB, int kWarps>
+__global__ void __launch_bounds__(32 * (kWarps + 1), 1)
+    q4_scores_kernel(const __grid_constant__ CUtensorMap tmQ, const Q4Args A) {
+  constexpr int kRows = 16 * kMT;                    // labels of a warp
+  constexpr int kTile = kRows * kWarps;              // labels of a tile
+  constexpr uint32_t kStage = kTile * kQKB;
+  constexpr int kWords = kG / 32;                    // words of 8 codes a thread has of a group and row
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int ng = A.d / kG;                           // groups of a label
+  uint4* xs = reinterpret_cast<uint4*>(ring + (size_t)A.stages * kStage);          // [ng * kWords][kNB][32]
+  uint16_t* sc = reinterpret_cast<uint16_t*>(xs + (size_t)ng * kWords * kNB * 32); // [2][kTile][ng]
+  SmemQ* S = reinterpret_cast<SmemQ*>(sc + (size_t)2 * kTile * ng);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int b0 = blockIdx.y * 8 * kNB;
+  const int64_t T = (A.L + kTile - 1) / kTile;
+  const int nkb = (A.d / 2 + kQKB - 1) / kQKB;
+  volatile int* abort = &S->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < A.stages; ++s) { mbar_init(&S->full[s], 1); mbar_init(&S->empty[s], kWarps); }
+    S->abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    if (elect_one()) {
+      tma_prefetch_desc(&tmQ);
+      uint32_t it = 0;
+      for (int64_t tile = blockIdx.x; tile < T && !*abort; tile += gridDim.x) {
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = (int)(it % (uint32_t)A.stages);
+          const uint32_t ph = (it / (uint32_t)A.stages) & 1;
+          if (!mbar_wait(&S->empty[s], ph ^ 1, abort, kQWait)) { *abort = 1; break; }
+          mbar_arrive_expect_tx(&S->full[s], kStage);
+          tma_load_2d(ring + (size_t)s * kStage, &tmQ, &S->full[s], kb * kQKB, (int32_t)(tile * kTile));
+        }
+      }
+    }
+  }
+
+  // X into fragment order.  The exponents first: warp w takes queries w, w + kWarps, ...
+  if (warp < kWarps) {
+    for (int n = warp; n < 8 * kNB; n += kWarps) {
+      uint32_t m = 0;
+      if (b0 + n < A.B) {
+        const uint4* xr = reinterpret_cast<const uint4*>(A.X + (size_t)(b0 + n) * A.d);
+        for (int j = lane; j < A.d / 8; j += 32) {
+          const uint4 v = xr[j];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+            if (lo < 0x7F80u) m = max(m, lo);          // the largest finite magnitude
+            if (hi < 0x7F80u) m = max(m, hi);
+          }
+        }
+        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      }
+      if (lane == 0) S->exponent[n] = m == 0 ? 0 : 141 - max((int)(m >> 7), 1);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    const int nf = ng * kWords * kNB * 32;
+    for (int f = threadIdx.x; f < nf; f += 32 * kWarps) {
+      const int ln = f & 31, nb = (f >> 5) % kNB, jw = (f >> 5) / kNB;
+      const int j = jw / kWords, w = jw % kWords;
+      const int n = nb * 8 + (ln >> 2);
+      uint4 o = make_uint4(0u, 0u, 0u, 0u);
+      if (b0 + n < A.B) {
+        const int k = j * kG + (ln & 3) * (kG / 4) + 8 * w;
+        const uint4 v = *reinterpret_cast<const uint4*>(A.X + (size_t)(b0 + n) * A.d + k);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const int e = S->exponent[n];
+        __half h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[2 * i] = __float2half_rn(ldexpf(__uint_as_float(x[i] << 16), e));
+          h[2 * i + 1] = __float2half_rn(ldexpf(__uint_as_float(x[i] & 0xFFFF0000u), e));
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 q = __halves2half2(h[i], h[i + 4]);
+          p[i] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        o = make_uint4(p[0], p[1], p[2], p[3]);
+      }
+      xs[f] = o;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+
+    // the scales of this warp's labels of a tile: one run of 2 ng kRows bytes
+    // (a multiple of 16, as its start is), cut at the matrix's end
+    uint16_t* my_sc = sc + (size_t)warp * kRows * ng;
+    auto fetch_scales = [&](int64_t tile, int buf) {
+      const int64_t l0 = tile * kTile + (int64_t)warp * kRows;
+      const int64_t end = A.L * ng * 2;
+      const uint32_t dst = smem_u32(my_sc + (size_t)buf * kTile * ng);
+      for (int c = lane; c < kRows * ng / 8; c += 32) {
+        const int64_t off = l0 * ng * 2 + (int64_t)c * 16;
+        const int64_t left = end - off;
+        const uint32_t n = left >= 16 ? 16u : (left > 0 ? (uint32_t)left : 0u);
+        cp_async16(dst + c * 16, reinterpret_cast<const uint8_t*>(A.scales) + (n ? off : 0), n);
+      }
+      cp_async_commit();
+    };
+    if ((int64_t)blockIdx.x < T) fetch_scales(blockIdx.x, 0);
+
+    uint32_t it = 0;
+    int buf = 0;
+    const int row0 = warp * kRows + q4_row<kG>(g);     // of the tile: fragment rows g, g + 8 are rows row0, row0 + 8
+    for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x, buf ^= 1) {
+      cp_async_wait();
+      __syncwarp();
+      if (tile + gridDim.x < T) fetch_scales(tile + gridDim.x, buf ^ 1);
+      float out[kMT][kNB][4];
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[m][nb][e] = 0.0f;
+      const uint16_t* ts = sc + (size_t)buf * kTile * ng + (size_t)row0 * ng;
+      bool ok = true;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int s = (int)(it % (uint32_t)A.stages);
+        const uint32_t ph = (it / (uint32_t)A.stages) & 1;
+        if (!mbar_wait(&S->full[s], ph, abort, kQWait)) { *abort = 1; ok = false; break; }
+        const uint32_t st = smem_u32(ring) + (uint32_t)s * kStage + (uint32_t)row0 * kQKB;
+        const int j1 = min(2 * kQKB / kG, ng - kb * (2 * kQKB / kG));
+#pragma unroll 2
+        for (int j = 0; j < j1; ++j) {
+          const int gi = kb * (2 * kQKB / kG) + j;
+          float acc[kMT][kNB][4];
+#pragma unroll
+          for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[m][nb][e] = 0.0f;
+          const uint32_t byte = (uint32_t)(j * (kG / 2) + t * (kG / 8));
+          // rows row0 + 8 i share row & 7: the same swizzle
+          const uint32_t at = (((byte >> 4) ^ (uint32_t)(row0 & 7)) << 4) | (byte & 15u);
+          uint32_t c[2 * kMT][kWords];
+#pragma unroll
+          for (int r = 0; r < 2 * kMT; ++r) lds_words<kWords>(st + at + (uint32_t)(r * 8 * kQKB), c[r]);
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            uint4 x[kNB];
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) x[nb] = xs[(((size_t)gi * kWords + w) * kNB + nb) * 32 + lane];
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) {
+              uint32_t p[4], q[4];
+              q4_pairs(c[2 * m][w], p);
+              q4_pairs(c[2 * m + 1][w], q);
+#pragma unroll
+              for (int nb = 0; nb < kNB; ++nb) {
+                mma_f16(acc[m][nb], p[0], q[0], p[1], q[1], x[nb].x, x[nb].y);
+                mma_f16(acc[m][nb], p[2], q[2], p[3], q[3], x[nb].z, x[nb].w);
+              }
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < kMT; ++m) {
+            const float s0 = bf16_to_f32(ts[(size_t)(16 * m) * ng + gi]);
+            const float s1 = bf16_to_f32(ts[(size_t)(16 * m + 8) * ng + gi]);
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb) {
+              out[m][nb][0] = __fmaf_rn(s0, acc[m][nb][0], out[m][nb][0]);
+              out[m][nb][1] = __fmaf_rn(s0, acc[m][nb][1], out[m][nb][1]);
+              out[m][nb][2] = __fmaf_rn(s1, acc[m][nb][2], out[m][nb][2]);
+              out[m][nb][3] = __fmaf_rn(s1, acc[m][nb][3], out[m][nb][3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S->empty[s]);
+      }
+      if (!ok) {        // a wait ran out: no score of the tiles left is valid
+        for (int64_t tl = tile; tl < T; tl += gridDim.x)
+          for (int r = lane; r < kRows; r += 32)
+            for (int n = b0; n < min(b0 + 8 * kNB, A.B); ++n)
+              if (tl * kTile + warp * kRows + r < A.L) A.Z[(int64_t)n * A.ldz + tl * kTile + warp * kRows + r] = NAN;
+        break;
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = nb * 8 + 2 * t + c;
+          if (b0 + n >= A.B) continue;
+          const int e = -S->exponent[n];
+          // 2^e in two factors, each a normal number
+          const float f0 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
+          const float f1 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
+          float* z = A.Z + (int64_t)(b0 + n) * A.ldz;
+#pragma unroll
+          for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int64_t l = tile * kTile + row0 + 16 * m + 8 * h;
+              if (l < A.L) __stcs(z + l, out[m][nb][2 * h + c] * f0 * f1);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort) __nanosleep(20000);       // copies still in flight land before the shared memory is given up
+}
+
+template <int kG, int kMT, int kNB, int kWarps>
+cudaError_t run_q4(const uint8_t* codes, Q4Args A, int sms, cudaStream_t s) {
+  constexpr int kTile = 16 * kMT * kWarps;
+  constexpr size_t kStage = (size_t)kTile * kQKB;
+  const size_t fixed = 1024 + (size_t)(A.d / 8) * kNB * 128 + (size_t)4 * kTile * (A.d / kG) + sizeof(SmemQ);
+  int stages = (int)((kQSmem - fixed) / kStage);
+  const int64_t T = (A.L + kTile - 1) / kTile;
+  const int64_t boxes = (A.d / 2 + kQKB - 1) / kQKB * ((T + sms - 1) / sms);
+  if (stages > kQMaxStages) stages = kQMaxStages;
+  if (stages > boxes) stages = (int)boxes;
+  A.stages = stages;
+  const size_t smem = fixed + (size_t)stages * kStage;
+  CUtensorMap tm;
+  cudaError_t e = make_tma_map_2d(&tm, codes, 1, (uint64_t)A.d / 2, (uint64_t)A.L, (uint64_t)A.d / 2, kTile);
+  if (e != cudaSuccess) return e;
+  auto k = q4_scores_kernel<kG, kMT, kNB, kWarps>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQSmem)) != cudaSuccess) return e;
+  const dim3 grid((unsigned)(T < sms ? T : sms), (unsigned)((A.B + 8 * kNB - 1) / (8 * kNB)));
+  k<<<grid, 32 * (kWarps + 1), smem, s>>>(tm, A);
+  return cudaGetLastError();
+}
+
+template <int kG>
+cudaError_t run_q4_group(const uint8_t* codes, const Q4Args& A, cudaStream_t s) {
+  const int sms = device_sms();
+  // queries of one pass over the codes: as many as the fragments of X leave room for
+  const int nb = (A.B + 7) / 8;
+  const size_t x1 = (size_t)A.d * 16;                // X fragments of 8 queries
+  const int most = (int)((64 * 1024) / x1) < 1 ? 1 : (int)((64 * 1024) / x1);
+  const int want = nb < most ? nb : most;
+  if (want >= 4) return run_q4<kG, 1, 4, 8>(codes, A, sms, s);
+  if (want >= 2) return run_q4<kG, 1, 2, 8>(codes, A, sms, s);
+  return run_q4<kG, 1, 1, 8>(codes, A, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_q4_pack(const void* W, int64_t L, int32_t d, int w_format, int32_t group, uint8_t* codes,
+                           uint16_t* scales, cudaStream_t s) {
+  const int64_t n16 = L * d / 16;
+  const int grid = flat_grid(n16), lanes = group / 16;
+  uint2* c = reinterpret_cast<uint2*>(codes);
+  if (w_format == ELMO_BF16) q4_pack_kernel<ELMO_BF16><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
+  else if (w_format == ELMO_FP8_E5M2) q4_pack_kernel<ELMO_FP8_E5M2><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
+  else q4_pack_kernel<ELMO_FP8_E4M3><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_q4_unpack(const uint8_t* codes, const uint16_t* scales, int64_t L, int32_t d, int32_t group,
+                             uint16_t* W, cudaStream_t s) {
+  const int64_t n16 = L * d / 16;
+  q4_unpack_kernel<<<flat_grid(n16), kPackThreads, 0, s>>>(reinterpret_cast<const uint2*>(codes), scales, n16,
+                                                           group / 16, reinterpret_cast<uint4*>(W));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_q4_scores(const uint8_t* codes, const uint16_t* scales, int64_t L, int32_t d, int32_t group,
+                             const uint16_t* X, int32_t B, float* Z, int64_t ldz, cudaStream_t s) {
+  const Q4Args A{scales, X, Z, L, ldz, d, B, 0};
+  if (group == 32) return run_q4_group<32>(codes, A, s);
+  if (group == 64) return run_q4_group<64>(codes, A, s);
+  return run_q4_group<128>(codes, A, s);
+}
+
+}  // namespace elmo

@@ -82,3 +82,24 @@ def test_calls_on_a_null_head(lib):
     assert lib.elmo_train_step_chunked(None, DEV, 4, DEV, DEV, 3, 0.1, 128, 0, 0, DEV, None) == EINVAL
     assert lib.elmo_topk_predict(None, DEV, 4, 5, 128, DEV, DEV, None) == EINVAL
     assert lib.elmo_head_destroy(None) == OK
+
+
+def test_q4_arguments(lib):
+    def scores(codes=DEV, scales=DEV, L=100, d=128, group=64, X=DEV, B=4, Z=DEV, ldz=100):
+        return lib.elmo_q4_scores(codes, scales, L, d, group, X, B, Z, ldz, None)
+
+    assert scores(codes=None) == EINVAL and scores(scales=None) == EINVAL and scores(X=None) == EINVAL
+    assert scores(Z=None) == EINVAL
+    assert scores(codes=DEV + 8) == EINVAL and scores(scales=DEV + 2) == EINVAL and scores(X=DEV + 2) == EINVAL
+    assert scores(Z=DEV + 2) == EINVAL and "aligned" in _err(lib)
+    assert scores(L=0) == EINVAL and scores(L=1 << 24, ldz=1 << 24) == EINVAL
+    assert scores(d=32) == EINVAL and scores(d=96) == EINVAL and scores(d=8192) == EINVAL
+    assert scores(group=16) == EINVAL and scores(group=0) == EINVAL and scores(group=256) == EINVAL
+    assert scores(d=64, group=128) == EINVAL and "multiple" in _err(lib)
+    assert scores(B=0) == EINVAL and scores(B=4097) == EINVAL
+    assert scores(ldz=99) == EINVAL
+    assert lib.elmo_q4_pack(DEV, 100, 128, 9, 64, DEV, DEV, None) == EINVAL and "dtype" in _err(lib)
+    assert lib.elmo_q4_pack(None, 100, 128, 0, 64, DEV, DEV, None) == EINVAL
+    assert lib.elmo_q4_pack(DEV, 100, 128, 0, 48, DEV, DEV, None) == EINVAL
+    assert lib.elmo_q4_unpack(DEV, DEV, 100, 128, 64, DEV + 4, None) == EINVAL
+    assert lib.elmo_q4_unpack(DEV, DEV, -1, 128, 64, DEV, None) == EINVAL
