@@ -476,6 +476,76 @@ elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_
 elmo_status elmo_q4_scores(const void* codes_dev, const void* scales_dev, int64_t L, int32_t d, int32_t group,
                            const void* X_dev, int32_t B, float* Z_dev, int64_t ldz, void* stream);
 
+/* Element type of a matrix of scores (elmo_score_logprobs and its gradient). */
+typedef enum {
+  ELMO_SCORE_F32 = 0,
+  ELMO_SCORE_BF16 = 1
+} elmo_score_dtype;
+
+/*
+ * elmo_score_logprobs -- log probabilities of given labels, log-sum-exp,
+ * entropy and the k best labels of rows of scores.
+ *
+ * Passage: the head scores every label (atlas summary, "Approach"); here a
+ * row of scores z is read as the logits of a softmax over the labels:
+ *     lse = log sum_l e^(z_l),  log p_l = z_l - lse,  H = -sum_l p_l log p_l,
+ * in one pass with a running maximum; sums in fp32 over runs of a row, joined
+ * in 64 bits.  A score of -inf masks its label: its log p is -inf, and it is
+ * never listed.  A row with every label masked has lse = -inf, H = 0 and
+ * log p = -inf.  A row holding a NaN has NaN statistics; one holding +inf
+ * has lse = +inf and H = NaN.
+ *
+ *   Z_dev      : [B x L] scores of type zt, row b at element b * ldz
+ *                (ldz >= L); any alignment of its elements.
+ *   B, L       : 1 <= B <= ELMO_MAX_PREDICT_BATCH, 1 <= L < ELMO_MAX_LABELS.
+ *   rowptr_dev : int32 [B + 1], cols_dev int32 [nnz]: the given labels of each
+ *                row (CSR), in any order, a label possibly more than once.
+ *                Entries outside [0, nnz) are not read.
+ *   k          : 0 <= k <= min(L, ELMO_MAX_TOPK) labels listed.
+ *   logp_dev   : fp32 [nnz], written: log p of each given label; NaN where
+ *                the label id is outside [0, L).
+ *   lse_dev, entropy_dev : fp32 [B], written.
+ *   top_idx_dev, top_logp_dev : int32 / fp32 [B x k], written: the labels with
+ *                the largest scores, best first, ties to the lower label, and
+ *                their log p; -1 and -inf beyond the labels that are neither
+ *                masked nor NaN.  May be NULL with k = 0.
+ *   work_dev, work_bytes : device memory of at least
+ *                elmo_score_logprobs_workspace_bytes bytes, 16-byte aligned,
+ *                of any content; calls that may overlap need their own.
+ */
+elmo_status elmo_score_logprobs(const void* Z_dev, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L,
+                                const int32_t* rowptr_dev, const int32_t* cols_dev, int32_t nnz, int32_t k,
+                                float* logp_dev, float* lse_dev, float* entropy_dev, int32_t* top_idx_dev,
+                                float* top_logp_dev, void* work_dev, size_t work_bytes, void* stream);
+
+/* Bytes of workspace that elmo_score_logprobs(B, L, k) needs (host only). */
+elmo_status elmo_score_logprobs_workspace_bytes(int32_t B, int64_t L, int32_t k, size_t* bytes);
+
+/*
+ * elmo_score_logprobs_backward -- the gradient with regard to the scores.
+ *
+ * With g_i the gradient of the log p of the row's given label c_i, and g_lse
+ * and g_H those of its lse and entropy:
+ *     dz_l = sum_{i: c_i = l} g_i + p_l (g_lse - sum_i g_i - g_H (log p_l + H)),
+ * in fp32, rounded once to the scores' type.  A label given several times gets
+ * the sum in the order of the list.  Given labels outside [0, L) count for
+ * nothing; a row whose lse is infinite has a zero gradient.  The k best labels
+ * carry no gradient.
+ *
+ *   Z_dev ... nnz : as in elmo_score_logprobs.
+ *   lse_dev, entropy_dev : its outputs; entropy_dev may be NULL with g_entropy_dev.
+ *   g_logp_dev : fp32 [nnz] or NULL;  g_lse_dev, g_entropy_dev : fp32 [B] or NULL
+ *                (NULL = zeros).
+ *   dZ_dev     : [B x L] of type zt, row b at element b * lddz (lddz >= L),
+ *                written; may be Z_dev itself (with the same pitch), must not
+ *                overlap it otherwise.
+ */
+elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L,
+                                         const int32_t* rowptr_dev, const int32_t* cols_dev, int32_t nnz,
+                                         const float* lse_dev, const float* entropy_dev, const float* g_logp_dev,
+                                         const float* g_lse_dev, const float* g_entropy_dev, void* dZ_dev,
+                                         int64_t lddz, void* stream);
+
 /* Message of the most recent failure on the calling thread ("" if none). */
 const char* elmo_last_error(void);
 

@@ -11,7 +11,8 @@ The names match the C entry points:
   elmo_train_step_chunked, elmo_train_step_noalloc, elmo_forward_chunk,
   elmo_topk_predict, elmo_topk_merge, elmo_sr_round, elmo_sr_draws,
   elmo_precision_at_k, elmo_kahan_sgd, elmo_round_bf16,
-  elmo_q4_pack, elmo_q4_unpack, elmo_q4_scores,
+  elmo_q4_pack, elmo_q4_unpack, elmo_q4_scores, elmo_score_logprobs,
+  elmo_score_logprobs_workspace_bytes, elmo_score_logprobs_backward,
   elmo_check_bounded_wait, elmo_sync_status,
   elmo_head_workspace_bytes and the tracing calls.
 """
@@ -33,6 +34,7 @@ __all__ = [
     "elmo_check_bounded_wait", "WAIT_CHECK_SITE", "elmo_precision_at_k", "elmo_init_head_shard",
     "elmo_topk_merge", "MAX_SHARDS", "MAX_TOTAL_LABELS", "elmo_kahan_sgd", "elmo_round_bf16", "elmo_last_error",
     "elmo_q4_pack", "elmo_q4_unpack", "elmo_q4_scores",
+    "elmo_score_logprobs", "elmo_score_logprobs_workspace_bytes", "elmo_score_logprobs_backward",
 ]
 
 BF16 = 0
@@ -111,6 +113,10 @@ def _declare(L):
     L.elmo_q4_pack.argtypes = [P, i64, i32, ctypes.c_int, i32, P, P, P]
     L.elmo_q4_unpack.argtypes = [P, P, i64, i32, i32, P, P]
     L.elmo_q4_scores.argtypes = [P, P, i64, i32, i32, P, i32, P, i64, P]
+    L.elmo_score_logprobs.argtypes = [P, ctypes.c_int, i64, i32, i64, P, P, i32, i32, P, P, P, P, P, P,
+                                      ctypes.c_size_t, P]
+    L.elmo_score_logprobs_workspace_bytes.argtypes = [i32, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+    L.elmo_score_logprobs_backward.argtypes = [P, ctypes.c_int, i64, i32, i64, P, P, i32, P, P, P, P, P, P, i64, P]
     for name in ("elmo_profile_enable", "elmo_profile_reset", "elmo_profile_read", "elmo_launch_count","elmo_init_head", "elmo_head_destroy", "elmo_train_step_chunked", "elmo_forward_chunk",
                  "elmo_topk_predict", "elmo_sr_round", "elmo_sr_draws", "elmo_sync_status",
                  "elmo_head_workspace_bytes", "elmo_topk_uncertified_rows", "elmo_topk_screen_scores"):
@@ -394,6 +400,79 @@ def elmo_q4_scores(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, Z
     _here(codes, scales, X, Z)
     z, ldz = _rows_ptr("Z", Z)
     _check(load().elmo_q4_scores(_ptr(codes), _ptr(scales), L, d, group, _ptr(X), B, z, ldz, _stream(stream)))
+
+
+_SCORE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _given(rowptr, cols, B):
+    _shape("rowptr", rowptr, (B + 1,), torch.int32)
+    _shape("cols", cols, (cols.numel(),), torch.int32)
+    return cols.numel()
+
+
+def _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp):
+    """Checks the outputs of a log-probability call; returns k."""
+    _shape("logp", logp, (nnz,), torch.float32)
+    _shape("lse", lse, (B,), torch.float32)
+    _shape("entropy", entropy, (B,), torch.float32)
+    if (top_idx is None) != (top_logp is None):
+        raise ValueError("top_idx and top_logp go together")
+    if top_idx is None:
+        return 0
+    k = top_idx.shape[-1]
+    _shape("top_idx", top_idx, (B, k), torch.int32)
+    _shape("top_logp", top_logp, (B, k), torch.float32)
+    return k
+
+
+def elmo_score_logprobs_workspace_bytes(B: int, L: int, k: int) -> int:
+    """Bytes of workspace that elmo_score_logprobs needs for B rows of L scores and k best labels."""
+    n = ctypes.c_size_t()
+    _check(load().elmo_score_logprobs_workspace_bytes(int(B), int(L), int(k), ctypes.byref(n)))
+    return int(n.value)
+
+
+def elmo_score_logprobs(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tensor, logp: torch.Tensor,
+                        lse: torch.Tensor, entropy: torch.Tensor, top_idx: torch.Tensor | None,
+                        top_logp: torch.Tensor | None, workspace: torch.Tensor, stream=None):
+    """Softmax statistics of rows of scores Z (fp32 or bf16 [B, L], rows may have a pitch): logp fp32 [nnz] of the
+    given labels (CSR rowptr / cols, int32), lse and entropy fp32 [B], and the k best labels top_idx int32 [B, k]
+    with top_logp fp32 [B, k] (None: no list).  workspace: any tensor of at least
+    elmo_score_logprobs_workspace_bytes(B, L, k) bytes; see include/elmo.h."""
+    B, L = Z.shape
+    _shape("Z", Z, (B, L), *_SCORE_TYPES)
+    nnz = _given(rowptr, cols, B)
+    k = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
+    _here(Z, rowptr, cols, logp, lse, entropy, top_idx, top_logp, workspace)
+    z, ldz = _rows_ptr("Z", Z)
+    _check(load().elmo_score_logprobs(z, _SCORE_TYPES[Z.dtype], ldz, B, L, _ptr(rowptr), _ptr(cols) if nnz else None,
+                                      nnz, k, _ptr(logp) if nnz else None, _ptr(lse), _ptr(entropy),
+                                      _ptr(top_idx) if k else None, _ptr(top_logp) if k else None, _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tensor, lse: torch.Tensor,
+                                 entropy: torch.Tensor | None, g_logp: torch.Tensor | None,
+                                 g_lse: torch.Tensor | None, g_entropy: torch.Tensor | None, dZ: torch.Tensor,
+                                 stream=None):
+    """dZ (Z's type and shape; may be Z) = the gradient of elmo_score_logprobs with regard to the scores, given the
+    gradients g_logp fp32 [nnz], g_lse and g_entropy fp32 [B] of its outputs (None: zeros) and its lse and entropy."""
+    B, L = Z.shape
+    _shape("Z", Z, (B, L), *_SCORE_TYPES)
+    _shape("dZ", dZ, (B, L), Z.dtype)
+    nnz = _given(rowptr, cols, B)
+    for name, t, n in (("lse", lse, B), ("entropy", entropy, B), ("g_logp", g_logp, nnz), ("g_lse", g_lse, B),
+                       ("g_entropy", g_entropy, B)):
+        if t is not None or name == "lse":
+            _shape(name, t, (n,), torch.float32)
+    _here(Z, rowptr, cols, lse, entropy, g_logp, g_lse, g_entropy, dZ)
+    z, ldz = _rows_ptr("Z", Z)
+    dz, lddz = _rows_ptr("dZ", dZ)
+    _check(load().elmo_score_logprobs_backward(z, _SCORE_TYPES[Z.dtype], ldz, B, L, _ptr(rowptr),
+                                               _ptr(cols) if nnz else None, nnz, _ptr(lse), _ptr(entropy),
+                                               _ptr(g_logp) if nnz else None, _ptr(g_lse), _ptr(g_entropy), dz, lddz,
+                                               _stream(stream)))
 
 
 def elmo_check_bounded_wait(limit_cycles: int, status: torch.Tensor, stream=None):

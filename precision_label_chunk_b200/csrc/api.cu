@@ -140,6 +140,20 @@ elmo_status check_q4(const void* codes, const void* scales, int64_t L, int32_t d
   return ELMO_OK;
 }
 
+// Rows of scores and the lists of given labels (elmo_score_*).
+elmo_status check_scores(const void* Z, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L, const int32_t* rowptr,
+                         const int32_t* cols, int32_t nnz) {
+  if (!Z || !rowptr) return fail(ELMO_EINVAL, "null Z or rowptr");
+  if (zt != ELMO_SCORE_F32 && zt != ELMO_SCORE_BF16) return fail(ELMO_EINVAL, "unknown score type %d", (int)zt);
+  if (reinterpret_cast<uintptr_t>(Z) % (zt == ELMO_SCORE_F32 ? 4 : 2)) return fail(ELMO_EINVAL, "Z is not aligned to its elements");
+  if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
+  if (L < 1 || L >= ELMO_MAX_LABELS) return fail(ELMO_EINVAL, "L = %lld outside [1, 2^24)", (long long)L);
+  if (ldz < L) return fail(ELMO_EINVAL, "pitch of Z = %lld below L = %lld", (long long)ldz, (long long)L);
+  if (nnz < 0) return fail(ELMO_EINVAL, "nnz = %d < 0", nnz);
+  if (nnz > 0 && !cols) return fail(ELMO_EINVAL, "null cols with nnz > 0");
+  return ELMO_OK;
+}
+
 }  // namespace
 
 namespace elmo {
@@ -600,6 +614,57 @@ elmo_status elmo_q4_scores(const void* codes_dev, const void* scales_dev, int64_
   ELMO_CUDA(elmo::launch_q4_scores(static_cast<const uint8_t*>(codes_dev), static_cast<const uint16_t*>(scales_dev), L,
                                    d, group, static_cast<const uint16_t*>(X_dev), B, Z_dev, ldz, as_stream(stream)),
             "q4_scores");
+  return ELMO_OK;
+}
+
+elmo_status elmo_score_logprobs_workspace_bytes(int32_t B, int64_t L, int32_t k, size_t* bytes) {
+  g_last_error.clear();
+  if (!bytes) return fail(ELMO_EINVAL, "null bytes");
+  if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
+  if (L < 1 || L >= ELMO_MAX_LABELS) return fail(ELMO_EINVAL, "L = %lld outside [1, 2^24)", (long long)L);
+  if (k < 0 || k > ELMO_MAX_TOPK || k > L) return fail(ELMO_EINVAL, "k = %d outside [0, min(L, %d)]", k, ELMO_MAX_TOPK);
+  *bytes = elmo::score_logprobs_workspace(B, L, k);
+  return ELMO_OK;
+}
+
+elmo_status elmo_score_logprobs(const void* Z_dev, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L,
+                                const int32_t* rowptr_dev, const int32_t* cols_dev, int32_t nnz, int32_t k,
+                                float* logp_dev, float* lse_dev, float* entropy_dev, int32_t* top_idx_dev,
+                                float* top_logp_dev, void* work_dev, size_t work_bytes, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  elmo_status st = check_scores(Z_dev, zt, ldz, B, L, rowptr_dev, cols_dev, nnz);
+  if (st != ELMO_OK) return st;
+  if (k < 0 || k > ELMO_MAX_TOPK || k > L) return fail(ELMO_EINVAL, "k = %d outside [0, min(L, %d)]", k, ELMO_MAX_TOPK);
+  if (!lse_dev || !entropy_dev || (nnz > 0 && !logp_dev) || (k > 0 && (!top_idx_dev || !top_logp_dev)))
+    return fail(ELMO_EINVAL, "null output");
+  const size_t need = elmo::score_logprobs_workspace(B, L, k);
+  if (!work_dev || !aligned16(work_dev) || work_bytes < need)
+    return fail(ELMO_EINVAL, "workspace null, not 16-byte aligned or below %zu bytes", need);
+  ELMO_CUDA(elmo::launch_score_logprobs(Z_dev, zt == ELMO_SCORE_BF16, ldz, B, L, rowptr_dev, cols_dev, nnz, k, logp_dev,
+                                        lse_dev, entropy_dev, top_idx_dev, top_logp_dev, work_dev, as_stream(stream)),
+            "score_logprobs");
+  return ELMO_OK;
+}
+
+elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L,
+                                         const int32_t* rowptr_dev, const int32_t* cols_dev, int32_t nnz,
+                                         const float* lse_dev, const float* entropy_dev, const float* g_logp_dev,
+                                         const float* g_lse_dev, const float* g_entropy_dev, void* dZ_dev,
+                                         int64_t lddz, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  elmo_status st = check_scores(Z_dev, zt, ldz, B, L, rowptr_dev, cols_dev, nnz);
+  if (st != ELMO_OK) return st;
+  if (!lse_dev) return fail(ELMO_EINVAL, "null lse");
+  if (g_entropy_dev && !entropy_dev) return fail(ELMO_EINVAL, "the entropy's gradient needs the entropy");
+  if (!dZ_dev || reinterpret_cast<uintptr_t>(dZ_dev) % (zt == ELMO_SCORE_F32 ? 4 : 2))
+    return fail(ELMO_EINVAL, "dZ null or not aligned to its elements");
+  if (lddz < L) return fail(ELMO_EINVAL, "pitch of dZ = %lld below L = %lld", (long long)lddz, (long long)L);
+  if (dZ_dev == Z_dev && lddz != ldz && B > 1) return fail(ELMO_EINVAL, "dZ in the place of Z needs its pitch");
+  ELMO_CUDA(elmo::launch_score_backward(Z_dev, zt == ELMO_SCORE_BF16, ldz, B, L, rowptr_dev, cols_dev, nnz, lse_dev,
+                                        entropy_dev, g_logp_dev, g_lse_dev, g_entropy_dev, dZ_dev, lddz,
+                                        as_stream(stream)), "score_logprobs_backward");
   return ELMO_OK;
 }
 

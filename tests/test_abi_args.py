@@ -103,3 +103,29 @@ def test_q4_arguments(lib):
     assert lib.elmo_q4_pack(DEV, 100, 128, 0, 48, DEV, DEV, None) == EINVAL
     assert lib.elmo_q4_unpack(DEV, DEV, 100, 128, 64, DEV + 4, None) == EINVAL
     assert lib.elmo_q4_unpack(DEV, DEV, -1, 128, 64, DEV, None) == EINVAL
+
+
+def test_score_logprobs_arguments(lib):
+    n = ctypes.c_size_t()
+    assert lib.elmo_score_logprobs_workspace_bytes(4, 1000, 5, ctypes.byref(n)) == OK and n.value > 0
+    need = n.value
+    assert lib.elmo_score_logprobs_workspace_bytes(4, 1000, 5, None) == EINVAL
+    assert lib.elmo_score_logprobs_workspace_bytes(4, 3, 4, ctypes.byref(n)) == EINVAL
+
+    def fwd(Z=DEV, zt=0, ldz=1000, B=4, L=1000, rowptr=DEV, cols=DEV, nnz=3, k=5, logp=DEV, lse=DEV, H=DEV, ti=DEV,
+            tl=DEV, work=DEV, wb=need):
+        return lib.elmo_score_logprobs(Z, zt, ldz, B, L, rowptr, cols, nnz, k, logp, lse, H, ti, tl, work, wb, None)
+
+    for bad in (dict(Z=None), dict(rowptr=None), dict(cols=None), dict(logp=None), dict(lse=None), dict(H=None),
+                dict(ti=None), dict(tl=None), dict(work=None), dict(zt=2), dict(zt=-1), dict(Z=DEV + 2), dict(zt=1, Z=DEV + 1),
+                dict(B=0), dict(B=4097), dict(L=0, ldz=0, k=0), dict(L=1 << 24, ldz=1 << 24), dict(ldz=999), dict(nnz=-1),
+                dict(k=-1), dict(k=65), dict(L=4), dict(work=DEV + 8), dict(wb=need - 1)):
+        assert fwd(**bad) == EINVAL, bad
+
+    def bwd(Z=DEV, zt=0, ldz=1000, B=4, L=1000, rowptr=DEV, cols=DEV, nnz=3, lse=DEV, H=DEV, g=DEV, gl=DEV, gH=DEV,
+            dZ=DEV + 64, lddz=1000):
+        return lib.elmo_score_logprobs_backward(Z, zt, ldz, B, L, rowptr, cols, nnz, lse, H, g, gl, gH, dZ, lddz, None)
+
+    for bad in (dict(Z=None), dict(dZ=None), dict(lse=None), dict(H=None), dict(dZ=DEV + 2), dict(lddz=999), dict(nnz=-2),
+                dict(zt=5), dict(dZ=DEV, lddz=1001)):
+        assert bwd(**bad) == EINVAL, bad
