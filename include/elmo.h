@@ -546,6 +546,40 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
                                          const float* g_lse_dev, const float* g_entropy_dev, void* dZ_dev,
                                          int64_t lddz, void* stream);
 
+/*
+ * elmo_label_logprobs -- the statistics of elmo_score_logprobs straight from
+ * the head: no score is stored.
+ *
+ * Passage: the label axis is processed in chunks so that no full logit matrix
+ * exists (atlas summary, "Approach").  The scores are z = x . w_l over all L
+ * labels of the head, X as its bf16 values.  The log-sum-exp and the entropy
+ * are formed from tensor-core scores (fp32 accumulation; in 8-bit heads X
+ * enters as a sum of two 8-bit numbers, which holds every bf16 value above
+ * about 2^-15 of its query's largest magnitude exactly); the scores of the
+ * given and of the listed labels are exact products summed in 64 bits, and the
+ * k best labels are those of these exact scores, ties to the lower label.
+ * (elmo_topk_predict ranks by an fp32 chain: the two lists may differ where
+ * scores agree to within fp32 rounding.)
+ *
+ *   X_dev      : bf16 [B x d] (device), 1 <= B <= ELMO_MAX_PREDICT_BATCH.  A
+ *                query holding a NaN or an infinity has NaN statistics and an
+ *                empty list (-1, -inf).
+ *   rowptr_dev, cols_dev, nnz, k, logp_dev, lse_dev, entropy_dev,
+ *   top_idx_dev, top_logp_dev : as in elmo_score_logprobs; a given label
+ *                outside [0, L) also sets ELMO_EDATA in the status word.
+ * Weights that are not finite count as the scores that they make (see
+ * elmo_score_logprobs).  Queries whose list the tensor-core scores cannot
+ * settle (ties, weights that are not finite) are ranked over all labels on the
+ * CUDA cores, which takes far longer.  ELMO_EUNSUPPORTED on a head made by
+ * elmo_init_head_shard that does not hold all labels.
+ * The workspace is the head's: the first call of a size allocates (call once
+ * before capturing into a CUDA graph); calls on one head must not overlap on
+ * the device.
+ */
+elmo_status elmo_label_logprobs(elmo_head* h, const void* X_dev, int32_t B, const int32_t* rowptr_dev,
+                                const int32_t* cols_dev, int32_t nnz, int32_t k, float* logp_dev, float* lse_dev,
+                                float* entropy_dev, int32_t* top_idx_dev, float* top_logp_dev, void* stream);
+
 /* Message of the most recent failure on the calling thread ("" if none). */
 const char* elmo_last_error(void);
 

@@ -13,6 +13,7 @@ The names match the C entry points:
   elmo_precision_at_k, elmo_kahan_sgd, elmo_round_bf16,
   elmo_q4_pack, elmo_q4_unpack, elmo_q4_scores, elmo_score_logprobs,
   elmo_score_logprobs_workspace_bytes, elmo_score_logprobs_backward,
+  elmo_label_logprobs,
   elmo_check_bounded_wait, elmo_sync_status,
   elmo_head_workspace_bytes and the tracing calls.
 """
@@ -35,6 +36,7 @@ __all__ = [
     "elmo_topk_merge", "MAX_SHARDS", "MAX_TOTAL_LABELS", "elmo_kahan_sgd", "elmo_round_bf16", "elmo_last_error",
     "elmo_q4_pack", "elmo_q4_unpack", "elmo_q4_scores",
     "elmo_score_logprobs", "elmo_score_logprobs_workspace_bytes", "elmo_score_logprobs_backward",
+    "elmo_label_logprobs",
 ]
 
 BF16 = 0
@@ -115,6 +117,7 @@ def _declare(L):
     L.elmo_q4_scores.argtypes = [P, P, i64, i32, i32, P, i32, P, i64, P]
     L.elmo_score_logprobs.argtypes = [P, ctypes.c_int, i64, i32, i64, P, P, i32, i32, P, P, P, P, P, P,
                                       ctypes.c_size_t, P]
+    L.elmo_label_logprobs.argtypes = [P, P, i32, P, P, i32, i32, P, P, P, P, P, P]
     L.elmo_score_logprobs_workspace_bytes.argtypes = [i32, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
     L.elmo_score_logprobs_backward.argtypes = [P, ctypes.c_int, i64, i32, i64, P, P, i32, P, P, P, P, P, P, i64, P]
     for name in ("elmo_profile_enable", "elmo_profile_reset", "elmo_profile_read", "elmo_launch_count","elmo_init_head", "elmo_head_destroy", "elmo_train_step_chunked", "elmo_forward_chunk",
@@ -473,6 +476,22 @@ def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: to
                                                _ptr(cols) if nnz else None, nnz, _ptr(lse), _ptr(entropy),
                                                _ptr(g_logp) if nnz else None, _ptr(g_lse), _ptr(g_entropy), dz, lddz,
                                                _stream(stream)))
+
+
+def elmo_label_logprobs(head: Head, X: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tensor, logp: torch.Tensor,
+                        lse: torch.Tensor, entropy: torch.Tensor, top_idx: torch.Tensor | None,
+                        top_logp: torch.Tensor | None, stream=None):
+    """The statistics of elmo_score_logprobs for queries X (bf16 [B, d]) against all labels of the head, without
+    storing a score: logp fp32 [nnz] of the given labels (CSR rowptr / cols), lse and entropy fp32 [B], the k best
+    labels top_idx int32 [B, k] with top_logp fp32 [B, k] (None: no list)."""
+    B = X.shape[0]
+    _shape("X", X, (B, head.d), *_BF16_BITS)
+    nnz = _given(rowptr, cols, B)
+    k = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
+    _here(X, rowptr, cols, logp, lse, entropy, top_idx, top_logp)
+    _check(load().elmo_label_logprobs(head.handle, _ptr(X), B, _ptr(rowptr), _ptr(cols) if nnz else None, nnz, k,
+                                      _ptr(logp) if nnz else None, _ptr(lse), _ptr(entropy),
+                                      _ptr(top_idx) if k else None, _ptr(top_logp) if k else None, _stream(stream)))
 
 
 def elmo_check_bounded_wait(limit_cycles: int, status: torch.Tensor, stream=None):

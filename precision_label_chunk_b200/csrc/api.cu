@@ -9,6 +9,7 @@
 #include <cstdlib>
 #include <new>
 #include <string>
+#include <vector>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -17,6 +18,15 @@
 #include "elmo_operators.h"
 
 namespace {
+
+// A head as this file allocates it: elmo_head and the workspace of
+// elmo_label_logprobs.  A workspace that became too small is kept until the
+// head goes: a captured graph may still use it.
+struct HeadImpl : elmo_head {
+  void* lp = nullptr;
+  size_t lp_bytes = 0, lp_held = 0;
+  std::vector<void*> lp_old;
+};
 
 // An NVTX range named after the entry point around each call, so that a
 // profiler's timeline groups the kernels of a call under the call's name.
@@ -114,6 +124,22 @@ elmo_status ensure_cand(elmo_head* h, size_t bytes) {
     return fail(ELMO_ENOMEM, "cannot allocate %zu bytes of top-k workspace", bytes);
   }
   h->cand_bytes = bytes;
+  return ELMO_OK;
+}
+
+// Grows by doubling, so that what is held stays below four times what is used.
+elmo_status ensure_lp(HeadImpl* h, size_t bytes) {
+  if (h->lp_bytes >= bytes) return ELMO_OK;
+  const size_t want = bytes > 2 * h->lp_bytes ? bytes : 2 * h->lp_bytes;
+  void* p = nullptr;
+  if (cudaMalloc(&p, want) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(ELMO_ENOMEM, "cannot allocate %zu bytes of log-probability workspace", want);
+  }
+  if (h->lp) h->lp_old.push_back(h->lp);
+  h->lp = p;
+  h->lp_bytes = want;
+  h->lp_held += want;
   return ELMO_OK;
 }
 
@@ -260,7 +286,7 @@ elmo_status elmo_init_head_shard(elmo_head** out, void* W_dev, int64_t L, int32_
   ELMO_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev), "cudaDeviceGetAttribute");
   if (major != 10) return fail(ELMO_EUNSUPPORTED, "device %d has compute capability %d.x; this library is built for sm_100a", dev, major);
   ELMO_CUDA(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute");
-  elmo_head* h = new (std::nothrow) elmo_head();
+  HeadImpl* h = new (std::nothrow) HeadImpl();
   if (!h) return fail(ELMO_ENOMEM, "host allocation failed");
   h->W = W_dev;
   h->L = L;
@@ -308,7 +334,10 @@ elmo_status elmo_head_destroy(elmo_head* h) {
   ELMO_NVTX_RANGE();
   g_last_error.clear();
   if (!h) return ELMO_OK;
+  HeadImpl* hi = static_cast<HeadImpl*>(h);
   cudaDeviceSynchronize();
+  if (hi->lp) cudaFree(hi->lp);
+  for (void* p : hi->lp_old) cudaFree(p);
   if (h->gbuf) cudaFree(h->gbuf);
   if (h->ring) cudaFree(h->ring);
   if (h->cand) cudaFree(h->cand);
@@ -318,13 +347,13 @@ elmo_status elmo_head_destroy(elmo_head* h) {
   if (h->join) cudaEventDestroy(h->join);
   for (auto& r : h->prof_recs) { cudaEventDestroy(r.start); cudaEventDestroy(r.stop); }
   for (auto e : h->prof_pool) cudaEventDestroy(e);
-  delete h;
+  delete hi;
   return ELMO_OK;
 }
 
 elmo_status elmo_head_workspace_bytes(const elmo_head* h, size_t* bytes) {
   if (!h || !bytes) return fail(ELMO_EINVAL, "null argument");
-  *bytes = h->base_bytes + h->gbuf_bytes + h->ring_bytes + h->cand_bytes;
+  *bytes = h->base_bytes + h->gbuf_bytes + h->ring_bytes + h->cand_bytes + static_cast<const HeadImpl*>(h)->lp_held;
   return ELMO_OK;
 }
 
@@ -665,6 +694,31 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
   ELMO_CUDA(elmo::launch_score_backward(Z_dev, zt == ELMO_SCORE_BF16, ldz, B, L, rowptr_dev, cols_dev, nnz, lse_dev,
                                         entropy_dev, g_logp_dev, g_lse_dev, g_entropy_dev, dZ_dev, lddz,
                                         as_stream(stream)), "score_logprobs_backward");
+  return ELMO_OK;
+}
+
+elmo_status elmo_label_logprobs(elmo_head* h, const void* X_dev, int32_t B, const int32_t* rowptr_dev,
+                                const int32_t* cols_dev, int32_t nnz, int32_t k, float* logp_dev, float* lse_dev,
+                                float* entropy_dev, int32_t* top_idx_dev, float* top_logp_dev, void* stream) {
+  ELMO_NVTX_RANGE();
+  g_last_error.clear();
+  if (!h) return fail(ELMO_EINVAL, "null head");
+  if (!X_dev || !rowptr_dev) return fail(ELMO_EINVAL, "null X or rowptr");
+  if (!aligned16(X_dev)) return fail(ELMO_EINVAL, "X is not 16-byte aligned");
+  if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
+  if (nnz < 0) return fail(ELMO_EINVAL, "nnz = %d < 0", nnz);
+  if (nnz > 0 && !cols_dev) return fail(ELMO_EINVAL, "null cols with nnz > 0");
+  if (k < 0 || k > ELMO_MAX_TOPK || (int64_t)k > h->L) return fail(ELMO_EINVAL, "k = %d outside [0, min(L, %d)]", k, ELMO_MAX_TOPK);
+  if (!lse_dev || !entropy_dev || (nnz > 0 && !logp_dev) || (k > 0 && (!top_idx_dev || !top_logp_dev)))
+    return fail(ELMO_EINVAL, "null output");
+  if (h->labels_total != h->L) return fail(ELMO_EUNSUPPORTED, "a head that is split over devices");
+  elmo_status st = check_device(h);
+  if (st != ELMO_OK) return st;
+  HeadImpl* hi = static_cast<HeadImpl*>(h);
+  if ((st = ensure_lp(hi, elmo::label_logprobs_workspace(h, B, k))) != ELMO_OK) return st;
+  ELMO_CUDA(elmo::launch_label_logprobs(h, static_cast<const uint16_t*>(X_dev), B, rowptr_dev, cols_dev, nnz, k,
+                                        logp_dev, lse_dev, entropy_dev, top_idx_dev, top_logp_dev, hi->lp,
+                                        as_stream(stream)), "label_logprobs");
   return ELMO_OK;
 }
 

@@ -8,6 +8,8 @@
 
 #include "../../include/elmo.h"
 
+struct elmo_head;
+
 namespace elmo {
 
 // q4.cu
@@ -27,5 +29,11 @@ cudaError_t launch_score_backward(const void* Z, bool bf16, int64_t ldz, int32_t
                                   const int32_t* cols, int32_t nnz, const float* lse, const float* entropy,
                                   const float* g_logp, const float* g_lse, const float* g_entropy, void* dZ,
                                   int64_t lddz, cudaStream_t s);
+
+// label_logprobs.cu
+size_t label_logprobs_workspace(const elmo_head* h, int32_t B, int32_t k);
+cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, const int32_t* rowptr,
+                                  const int32_t* cols, int32_t nnz, int32_t k, float* logp, float* lse, float* entropy,
+                                  int32_t* top_idx, float* top_logp, void* work, cudaStream_t s);
 
 }  // namespace elmo

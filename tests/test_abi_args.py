@@ -129,3 +129,8 @@ def test_score_logprobs_arguments(lib):
     for bad in (dict(Z=None), dict(dZ=None), dict(lse=None), dict(H=None), dict(dZ=DEV + 2), dict(lddz=999), dict(nnz=-2),
                 dict(zt=5), dict(dZ=DEV, lddz=1001)):
         assert bwd(**bad) == EINVAL, bad
+
+
+def test_label_logprobs_arguments(lib):
+    assert lib.elmo_label_logprobs(None, DEV, 4, DEV, DEV, 3, 5, DEV, DEV, DEV, DEV, DEV, None) == EINVAL
+    assert "head" in _err(lib)
