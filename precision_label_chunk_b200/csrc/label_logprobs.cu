@@ -52,7 +52,8 @@ constexpr float kFloor = -200.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr int kJoinThreads = 512;
-constexpr int kMaxCand = 1024;            // kept scores that the join looks at
+constexpr int kMaxCand = 1024;            // kept scores that the join ranks
+constexpr int kGroups = 128;
 constexpr int kSegs = 74;                 // label segments of the exact path
 constexpr int kExactThreads = 256;
 constexpr int kExactChunk = 2048;
@@ -526,11 +527,11 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   extern __shared__ double dyn[];
   double* xs = dyn;                                    // [d] the query
   __shared__ double ex[kMaxCand];                      // exact scores of the ones ranked
-  __shared__ float cv[kMaxCand];                       // kept scores from tau up
+  __shared__ float cv[kMaxCand];                       // kept scores near the best
   __shared__ int32_t ci[kMaxCand];
   __shared__ double stat[2];
   __shared__ int count;
-  __shared__ float kth;
+  __shared__ float kth, low;
   constexpr int kW = kJoinThreads / 32;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool bad = A.rflag[b] != 0;
@@ -602,11 +603,34 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   const uint32_t tau_key = A.tau[b];
   const float tau = ord32_value(tau_key);
   const size_t base = (size_t)b * A.G * A.kp;
-  for (int i = tid; i < A.G * A.kp; i += kJoinThreads) {
+  const int nc = A.G * A.kp;
+  const float inv = A.xinv[b];
+  // 2 delta in the accumulators' units, rounded up; 2^-126 for subnormal partial sums
+  float delta = __fmul_ru(A.gamma, __fadd_ru(A.n1[b], A.r1[b]));
+  delta = __fmul_ru(__fadd_ru(delta, A.r1[b]), max_weight(*A.wmax, A.fmt));
+  const float two = __fdiv_ru(__fmul_ru(2.0f, __fadd_ru(delta, 0x1p-126f)), inv);
+  // of the ranges' lists, only what comes within 2 delta of the k-th best: the
+  // k-th best of kGroups groups' best is at most that
+  float best = -INFINITY;
+  for (int i = tid; i < nc; i += kJoinThreads)
+    if (A.cand_i[base + i] >= 0) best = fmaxf(best, A.cand_v[base + i]);
+  for (int o = 1; o < kJoinThreads / kGroups; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  if (tid % (kJoinThreads / kGroups) == 0) cv[tid / (kJoinThreads / kGroups)] = best;
+  if (tid == 0) low = -INFINITY;
+  __syncthreads();
+  if (tid < kGroups) {
+    const float mine = cv[tid];
+    int above = 0, same = 0;
+    for (int j = 0; j < kGroups; ++j) { above += cv[j] > mine; same += cv[j] == mine; }
+    if (above < A.k && above + same >= A.k) low = mine;
+  }
+  __syncthreads();
+  const float from = __fsub_rd(low, two);
+  for (int i = tid; i < nc; i += kJoinThreads) {
     const int32_t l = A.cand_i[base + i];
     if (l < 0) continue;
     const float v = A.cand_v[base + i];
-    if (v >= tau) {
+    if (v >= from || !(two < INFINITY)) {
       const int at = atomicAdd(&count, 1);
       if (at < kMaxCand) { cv[at] = v; ci[at] = l; }
     }
@@ -615,11 +639,6 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   __syncthreads();
   const int n = count;
   bool ok = n >= A.k && n <= kMaxCand;
-  const float inv = A.xinv[b];
-  // 2 delta in the accumulators' units, rounded up; 2^-126 for subnormal partial sums
-  float delta = __fmul_ru(A.gamma, __fadd_ru(A.n1[b], A.r1[b]));
-  delta = __fmul_ru(__fadd_ru(delta, A.r1[b]), max_weight(*A.wmax, A.fmt));
-  const float two = __fdiv_ru(__fmul_ru(2.0f, __fadd_ru(delta, 0x1p-126f)), inv);
   if (ok) {
     for (int i = tid; i < n; i += kJoinThreads) {      // the k-th best kept score, ties in any order
       const float v = cv[i];
