@@ -14,22 +14,29 @@
 //      units of the last place, which E5M2's 3 bits hold exactly down to its
 //      2^-16 spacing: only numbers below about 2^-15 of the query's largest
 //      are rounded at all, to within 2^-23 of it.
-//   2. score pass (tcgen05): 128 queries against a range of labels a CTA; each
+//   2. score pass (tcgen05): 128 queries against a range of labels a CTA; an
 //      epilogue thread has one query and keeps its running maximum m,
-//      s = sum e^(z - m), t = sum e^(z - m)(z - m), and the kp > k best scores.
-//   3. join: the ranges' sums in 64 bits, the given labels' scores recomputed
-//      exactly (products exact, sums in 64 bits), and the k best labels: every
-//      label outside the kept ones scores at most tau (the largest kept-list
-//      minimum), so if the k-th best of the kept exceeds tau by more than twice
-//      the error bound delta of the tensor-core scores, the k best are among
-//      the kept ones within 2 delta of it, which are ranked by exact scores.
-//   4. queries that this does not settle (ties within delta, weights that are
-//      not finite) rank all labels by exact scores on the CUDA cores.
+//      s = sum e^(z - m) and t = sum e^(z - m)(z - m).  For the list it only
+//      notes the maximum of every block of labels, which the running maximum
+//      needs anyway: keeping the best scores in the pass (a heap a query,
+//      limits shared between the ranges) was measured at 1.8 ms where the rest
+//      of the pass takes 1.0.
+//   3. join: the ranges' sums in 64 bits; the given labels' scores recomputed
+//      exactly (products exact, sums in 64 bits); and the k best labels.  Let
+//      low be at most the k-th best block maximum.  k labels score at least
+//      low on the tensor cores, so a label among the k best does so to within
+//      2 delta, delta the error bound of those scores: the blocks with a
+//      maximum of at least low - 2 delta hold all of the k best.  Their labels
+//      are scored again in fp32, which narrows them down the same way, and
+//      what is left is ranked by exact scores.
+//   4. queries with too many labels within 2 delta (ties), or a head that is
+//      not finite, rank all labels by exact scores on the CUDA cores.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
 // r1 the sum of what hi and lo leave, gamma = nsteps 2^-22: each of the nsteps
-// accumulating instructions is allowed 2^-22 of the magnitudes summed.  max|W|
-// is read off the tiles in shared memory by two spare warps.
+// accumulating instructions is allowed 2^-22 of the magnitudes summed (a
+// thirty-second of the fp32 sum's d terms and 5 joins are less).  max|W| is
+// read off the tiles in shared memory by two spare warps.
 #include <cuda.h>
 #include <float.h>
 
@@ -43,17 +50,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;             // warp 0 TMA, 1 MMA and TMEM, 2-5 epilogue, 6-7 max|W|
+constexpr int kThreads = 384;             // warp 0 TMA, 1 MMA and TMEM, 2-9 epilogue, 10-11 max|W|
 constexpr int kMaxStages = 16;
-constexpr int kNBuf = 2;                  // accumulator buffers
 constexpr uint32_t kAccCol = 384;         // first accumulator column where X lies in TMEM
 constexpr long long kWait = 4000000000LL; // ~2 s
-constexpr float kFloor = -200.0f;
+constexpr float kFloor = -200.0f;         // z - m where e^(z - m) is 0 in fp32
+constexpr float kNoLabel = -3.0e38f;      // a score that e^ takes to 0 and whose product with it is 0
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kSmemMost = 227 * 1024;
+constexpr size_t kMaxima = size_t(256) << 20;   // bytes of block maxima, about
 constexpr int kJoinThreads = 512;
-constexpr int kMaxCand = 1024;            // kept scores that the join ranks
-constexpr int kGroups = 128;
+constexpr int kGroups = 256;              // groups whose best give the lower bound on the k-th best
+constexpr int kMaxBlocks = 256;           // blocks that are scored again for a query,
+constexpr int kMaxNear = 4096;            // of their labels the ones near the k-th best in fp32,
+constexpr int kMaxExact = 1024;           // and of those the ones ranked by exact scores
+constexpr int kNearThreads = 256;
+constexpr int kNearAt = 8;                // labels that a warp scores at a time
 constexpr int kSegs = 74;                 // label segments of the exact path
 constexpr int kExactThreads = 256;
 constexpr int kExactChunk = 2048;
@@ -68,14 +80,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// floats and doubles as whole numbers of the same order; 0 is below all
-__device__ __forceinline__ uint32_t ord32(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float ord32_value(uint32_t k) {
-  return k == 0 ? -INFINITY : __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
+// Doubles as whole numbers of the same order;
 // 0 for scores that are never listed (-inf, NaN); -0 and 0 are the same score
 __device__ __forceinline__ uint64_t ord64(double f) {
   if (!(f > -INFINITY)) return 0ull;
@@ -88,19 +93,28 @@ __device__ __forceinline__ double ord64_value(uint64_t k) {
 
 struct Stat { float m, s, t; };
 
+struct Counts { uint32_t wmax; int32_t nfail, nitems; };
+
 struct Args {
   const uint16_t* X;
   const uint8_t *xa, *xb;                 // 8-bit heads: hi and lo codes [B][d]
   const void* W;
   int64_t L, label_base, labels_total;
-  int32_t d, B, G, k, kp, stages, nnz, fmt;
+  int32_t d, B, G, k, nnz, fmt;
+  int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
+  int32_t nblk, nblkp, pairs;             // blocks of a parity, with padding; tiles of a block
   float gamma;
   float *xinv, *n1, *r1;
-  int32_t *rflag, *nfail, *fail;
-  uint32_t *wmax, *tau;
-  float* cand_v;                          // [B][G][kp]
-  int32_t* cand_i;
-  Stat* part;                             // [B][G]
+  int32_t *rflag, *fail;
+  int32_t* done;                          // [B] segments of a failed query that are ranked
+  Counts* counts;
+  float* bmax;                            // [B][2][nblkp] maxima of the accumulators over blocks
+  int2* items;                            // (query, block) to be scored again, at most kMaxBlocks a query
+  int32_t *listed, *nnear;                  // [B] whether the query's blocks are listed; labels found near
+  float* near_v;                          // [B][kMaxNear] their fp32 scores
+  int32_t* near_l;
+  float* from;                            // [B] the fp32 score from which a label is near
+  Stat* part;                             // [B][2 G]
   uint64_t* seg_key;                      // [B][kSegs][k]
   int32_t* seg_i;
   const int32_t *rowptr, *cols;
@@ -109,6 +123,10 @@ struct Args {
   double* rowstat;                        // [B][2] m and log s (for the exact path)
   int32_t* status;
 };
+
+// Tiles of even and odd number go to two groups of epilogue warps.  Block i
+// of a parity is the `pairs` tiles 2 (i pairs + r) + parity, and a range is a
+// run of blocks of both parities.
 
 // ---------------------------------------------------------------- 1. operands
 constexpr int kPrepThreads = 128;
@@ -129,8 +147,8 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
   __shared__ uint32_t mx;
   const int b = blockIdx.x, tid = threadIdx.x;
   if (tid == 0) {
-    if (b == 0) { *A.wmax = 0; *A.nfail = 0; }
-    A.tau[b] = 0;
+    if (b == 0) *A.counts = {0u, 0, 0};
+    if (A.k > 0) A.done[b] = A.nnear[b] = 0;
     mx = 0;
   }
   __syncthreads();
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
 
 // ---------------------------------------------------------------- 2. score pass
 struct SmemP {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kNBuf], tempty[kNBuf];
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -198,71 +216,118 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   if (atomicCAS(status, 0, (int)ELMO_ETIMEOUT) == 0) status[1] = site;
 }
 
-// The kept scores of column r of a CTA: a heap with the smallest on top,
-// entry i at [i * 128 + r].
-__device__ __forceinline__ void heap_down(float* hv, int32_t* hl, int r, int i, int n) {
-  const float v = hv[i * 128 + r];
-  const int32_t l = hl[i * 128 + r];
-  for (int c = 2 * i + 1; c < n; c = 2 * i + 1) {
-    float cv = hv[c * 128 + r];
-    if (c + 1 < n && hv[(c + 1) * 128 + r] < cv) cv = hv[++c * 128 + r];
-    if (!(cv < v)) break;
-    hv[i * 128 + r] = cv;
-    hl[i * 128 + r] = hl[c * 128 + r];
-    i = c;
-  }
-  hv[i * 128 + r] = v;
-  hl[i * 128 + r] = l;
+// two fp32 operations an instruction
+struct f2 { uint64_t v; };
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-// Adds a score to the n kept ones (of at most kp); the new lower limit.
-__device__ __forceinline__ float heap_keep(float* hv, int32_t* hl, int r, int n, int kp, float v, int32_t l) {
-  if (n < kp) {
-    hv[n * 128 + r] = v;
-    hl[n * 128 + r] = l;
-    if (n + 1 < kp) return -INFINITY;
-    for (int i = kp / 2 - 1; i >= 0; --i) heap_down(hv, hl, r, i, kp);
-  } else {
-    hv[r] = v;
-    hl[r] = l;
-    heap_down(hv, hl, r, 0, kp);
+// A query's running softmax: scores are inv times the accumulators, m in the
+// accumulators' units, t = sum e^(z - m)(z - m) / inv.
+struct Soft {
+  float m = -INFINITY, s = 0.0f, t = 0.0f;
+  float c2, floor_v;                                   // inv log2(e); -200 / inv
+
+  // 32 accumulators; returns their maximum
+  __device__ __forceinline__ float add32(const uint32_t (&v)[32]) {
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      x[c] = fmaxf(fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 8])),
+                   fmaxf(__uint_as_float(v[c + 16]), __uint_as_float(v[c + 24])));
+    const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (mx > m) {
+      if (m > -INFINITY) {
+        const float dm = fmaxf(m - mx, floor_v), c = ex2(dm * c2);
+        t = c * fmaf(s, dm, t);
+        s *= c;
+      }
+      m = mx;
+    }
+    const float m0 = m > -INFINITY ? m : 0.0f;
+    const f2 nm = pair(-m0, -m0), cc = pair(c2, c2);
+    f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const f2 d = add2(pair(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), nm);
+      float a, b;
+      unpair(mul2(d, cc), a, b);
+      const f2 e = pair(ex2(a), ex2(b));
+      ps[c & 1] = add2(ps[c & 1], e);
+      pt[c & 1] = fma2(e, d, pt[c & 1]);
+    }
+    float s0, s1, t0, t1;
+    unpair(add2(ps[0], ps[1]), s0, s1);
+    unpair(add2(pt[0], pt[1]), t0, t1);
+    float tt = t0 + t1;
+    if (tt != tt) {                                    // a score of -inf (0 times infinity), or a NaN
+      tt = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float d = max_nan(__uint_as_float(v[c]) - m0, floor_v);
+        tt = fmaf(ex2(d * c2), d, tt);
+      }
+    }
+    s += s0 + s1;
+    t += tt;
+    return mx;
   }
-  return hv[r];
-}
+};
 
 // kFp8: 8-bit head (kW5: E5M2 weights).  kXs = 0: d <= 768, X (two 8-bit or
 // one bf16 operand, 2 d bytes a query) stays in TMEM columns 0..383 and tiles
 // are 64 labels with two accumulators in the rest; kXs = 1: wider heads, X
 // comes through the ring with W, tiles are 128 labels.
+//
+// A stage of the ring holds kbs 128-byte k-blocks of q tiles, up to 48 KB in
+// one TMA request: the rate of the copies follows the number of requests (the
+// 500K bf16 head streamed at 5.2 TB/s in 8 KB requests).
 template <int kFp8, int kW5, int kXs>
 __global__ void __launch_bounds__(kThreads, 1)
     label_score_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB, const Args A) {
   constexpr int kN = kXs ? 128 : 64;
   constexpr int kOps = kFp8 ? 2 : 1;
-  constexpr uint32_t kWBytes = kN * 128;
-  constexpr uint32_t kXBytes = kXs ? 128 * 128 * kOps : 0;
-  constexpr uint32_t kStage = kWBytes + kXBytes;
   constexpr int kKE = kFp8 ? 128 : 64;                 // elements of a 128-byte k-block
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* zs = reinterpret_cast<float*>(ring + (size_t)A.stages * kStage);      // [32][128]
-  float* hv = zs + 32 * 128;                                                   // [kp][128]
-  int32_t* hl = reinterpret_cast<int32_t*>(hv + (size_t)A.kp * 128);
-  SmemP* S = reinterpret_cast<SmemP*>(hl + (size_t)A.kp * 128);
+  const uint32_t slab = (uint32_t)A.q * kN * 128;      // a k-block of the stage's labels
+  const uint32_t wbytes = slab * (uint32_t)A.kbs;
+  const uint32_t stage = wbytes + (kXs ? (uint32_t)A.kbs * 16384u * kOps : 0u);
+  SmemP* S = reinterpret_cast<SmemP*>(ring + (size_t)A.stages * stage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = (A.B + 127) / 128;
   const int p = blockIdx.x % P, g = blockIdx.x / P;
   const int64_t T = (A.L + kN - 1) / kN;
-  const int64_t t0 = T * g / A.G, t1 = T * (g + 1) / A.G;
+  const int64_t blk0 = (int64_t)A.nblk * g / A.G, blk1 = (int64_t)A.nblk * (g + 1) / A.G;
+  const int64_t t0 = 2 * blk0 * A.pairs, t1 = min(T, 2 * blk1 * A.pairs);
   const int nkb = (A.d + kKE - 1) / kKE;
+  const int nst = (nkb + A.kbs - 1) / A.kbs;           // stages of a group of q tiles (1 where q > 1)
   const uint32_t opcols = (uint32_t)nkb * 32;
   volatile int* abort = &S->abort;
-  const bool scan = p == 0 && A.kp > 0;                // this CTA's range is scanned for max|W|
+  const bool scan = A.k > 0;                           // the ranges are scanned for max|W|
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < A.stages; ++s) { mbar_init(&S->full[s], 1); mbar_init(&S->empty[s], scan ? 3 : 1); }
-    for (int i = 0; i < kNBuf; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 4); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 4); }
     S->abort = 0;
     fence_barrier_init();
   }
@@ -274,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (!kXs) {
     if (warp >= 2 && warp < 6) {                       // query r of the panel into lane r
-      const int q = warp & 3, row = p * 128 + q * 32 + lane;
+      const int quad = warp & 3, row = p * 128 + quad * 32 + lane;
       const size_t rowbytes = (size_t)A.d * (kFp8 ? 1 : 2);
       for (int op = 0; op < kOps; ++op) {
         const uint8_t* src = (kFp8 ? (op ? A.xb : A.xa) : reinterpret_cast<const uint8_t*>(A.X)) + (size_t)row * rowbytes;
@@ -287,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row < A.B && off < rowbytes) w4 = *reinterpret_cast<const uint4*>(src + off);
             v[4 * u] = w4.x; v[4 * u + 1] = w4.y; v[4 * u + 2] = w4.z; v[4 * u + 3] = w4.w;
           }
-          tmem_st32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)op * opcols + c0, v);
+          tmem_st32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)op * opcols + c0, v);
         }
       }
       tmem_wait_st();
@@ -300,18 +365,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       tma_prefetch_desc(&tmW);
-      uint32_t it = 0;
-      for (int64_t t = t0; t < t1 && !*abort; ++t) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % (uint32_t)A.stages, ph = (it / (uint32_t)A.stages) & 1;
-          if (!mbar_wait(&S->empty[s], ph ^ 1, abort, kWait)) { record_timeout(A.status, abort, 71); break; }
-          uint8_t* st = ring + (size_t)s * kStage;
-          mbar_arrive_expect_tx(&S->full[s], kStage);
-          tma_load_2d(st, &tmW, &S->full[s], kb * kKE, (int32_t)(t * kN));
-          if (kXs) {
-            tma_load_2d(st + kWBytes, &tmA, &S->full[s], kb * kKE, p * 128);
-            if (kFp8) tma_load_2d(st + kWBytes + 16384, &tmB, &S->full[s], kb * kKE, p * 128);
+      uint32_t s = 0, ph = 1;
+      for (int64_t t = t0; t < t1 && !*abort; t += A.q) {
+        for (int st = 0; st < nst; ++st) {
+          if (!mbar_wait(&S->empty[s], ph, abort, kWait)) { record_timeout(A.status, abort, 71); break; }
+          uint8_t* at = ring + (size_t)s * stage;
+          uint64_t* bar = &S->full[s];
+          const int kb0 = st * A.kbs;
+          mbar_arrive_expect_tx(bar, stage);
+          if (A.kb3d) {
+            tma_load_3d(at, &tmW, bar, 0, (int32_t)(t * kN), kb0);
+            if (kXs) {
+              tma_load_3d(at + wbytes, &tmA, bar, 0, p * 128, kb0);
+              if (kFp8) tma_load_3d(at + wbytes + A.kbs * 16384, &tmB, bar, 0, p * 128, kb0);
+            }
+          } else {
+            for (int j = 0; j < A.kbs; ++j) {
+              tma_load_2d(at + j * slab, &tmW, bar, (kb0 + j) * kKE, (int32_t)(t * kN));
+              if (kXs) {
+                tma_load_2d(at + wbytes + j * 16384, &tmA, bar, (kb0 + j) * kKE, p * 128);
+                if (kFp8) tma_load_2d(at + wbytes + (A.kbs + j) * 16384, &tmB, bar, (kb0 + j) * kKE, p * 128);
+              }
+            }
           }
+          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
         }
       }
     }
@@ -320,163 +397,168 @@ __global__ void __launch_bounds__(kThreads, 1)
       // hi is E4M3 (format 0) and lo E5M2 (1); bf16 operands are format 1 of their kind
       const uint32_t idesc[2] = {kFp8 ? make_idesc(0, kW5, 0, 0, 128, kN) : make_idesc(1, 1, 0, 0, 128, kN),
                                  make_idesc(1, kW5, 0, 0, 128, kN)};
-      uint32_t it = 0, n = 0;
-      for (int64_t t = t0; t < t1 && !*abort; ++t, ++n) {
-        const uint32_t buf = n % kNBuf, use = n / kNBuf;
-        if (!mbar_wait(&S->tempty[buf], (use & 1) ^ 1, abort, kWait)) { record_timeout(A.status, abort, 72); break; }
-        tc_fence_after();
-        const uint32_t dcol = tmem + (kXs ? 0 : kAccCol) + buf * kN;
-        bool ok = true;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % (uint32_t)A.stages, ph = (it / (uint32_t)A.stages) & 1;
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < t1 && ok && !*abort; t += A.q) {
+        for (int st = 0; st < nst && ok; ++st) {
           if (!mbar_wait(&S->full[s], ph, abort, kWait)) { record_timeout(A.status, abort, 73); ok = false; break; }
           tc_fence_after();
-          const uint32_t ws = smem_u32(ring + (size_t)s * kStage);
-#pragma unroll
-          for (int op = 0; op < kOps; ++op) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {              // 32 bytes of K an instruction
-              const uint64_t bd = sw128_desc(ws + k * 32, 16, 1024);
-              const uint32_t more = (kb | op | k) != 0;
-              if (kXs) {
-                const uint64_t ad = sw128_desc(ws + kWBytes + op * 16384 + k * 32, 16, 1024);
-                if (kFp8) mma_e4m3(dcol, ad, bd, idesc[op], more);
-                else mma_bf16(dcol, ad, bd, idesc[0], more);
-              } else {
-                const uint32_t a = tmem + (uint32_t)op * opcols + (uint32_t)kb * 32 + (uint32_t)k * 8;
-                if (kFp8) mma_e4m3_ts(dcol, a, bd, idesc[op], more);
-                else mma_bf16_ts(dcol, a, bd, idesc[0], more);
+          const uint32_t ws = smem_u32(ring + (size_t)s * stage);
+          for (int j = 0; j < A.q && t + j < t1; ++j) {
+            const int64_t rel = t + j - t0;
+            const uint32_t buf = (uint32_t)rel & 1;
+            if (st == 0) {
+              if (!mbar_wait(&S->tempty[buf], (uint32_t)((rel >> 1) & 1) ^ 1, abort, kWait)) {
+                record_timeout(A.status, abort, 72);
+                ok = false;
+                break;
               }
+              tc_fence_after();
             }
-          }
-          mma_commit(&S->empty[s]);
-        }
-        if (!ok) break;
-        mma_commit(&S->tfull[buf]);
-      }
-    }
-  } else if (warp < 6) {
-    const int q = warp & 3, r = q * 32 + lane, row = p * 128 + r;
-    const bool live = row < A.B;
-    const float inv = live ? A.xinv[row] : 1.0f;       // scores are inv times the accumulators
-    const float c2 = inv * kLog2e, floor_v = kFloor / inv;
-    float m = -INFINITY, s = 0.0f, t = 0.0f;
-    float mine = -INFINITY;                            // the smallest kept score, once kp are kept
-    int n = 0;
-    uint32_t nt = 0;
-    for (int64_t tile = t0; tile < t1 && !*abort; ++tile, ++nt) {
-      const uint32_t buf = nt % kNBuf, use = nt / kNBuf;
-      if (!mbar_wait(&S->tfull[buf], use & 1, abort, kWait)) { record_timeout(A.status, abort, 74); break; }
-      tc_fence_after();
-      float limit = A.kp > 0 && live ? fmaxf(mine, ord32_value(__ldcg(A.tau + row))) : INFINITY;
-#pragma unroll 1
-      for (int u = 0; u < kN / 64; ++u) {
-        uint32_t v[2][32];
-        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (kXs ? 0 : kAccCol) + buf * kN + u * 64;
-        tmem_ld32(at, v[0]);
-        tmem_ld32(at + 32, v[1]);
-        tmem_wait_ld();
-        if (u == kN / 64 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S->tempty[buf]);
-        }
-        if (!live) continue;
+            const uint32_t dcol = tmem + (kXs ? 0 : kAccCol) + buf * kN;
+            for (int i = 0; i < A.kbs && st * A.kbs + i < nkb; ++i) {
+              const int kb = st * A.kbs + i;
+              const uint32_t wk = ws + (uint32_t)i * slab + (uint32_t)j * (kN * 128);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t l0 = tile * kN + u * 64 + h * 32;
-          if (l0 + 32 > A.L) {                         // labels past the end are no labels
+              for (int op = 0; op < kOps; ++op) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (l0 + c >= A.L) v[h][c] = 0xFF800000u;
-          }
-          float x[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            x[c] = fmaxf(fmaxf(__uint_as_float(v[h][c]), __uint_as_float(v[h][c + 8])),
-                         fmaxf(__uint_as_float(v[h][c + 16]), __uint_as_float(v[h][c + 24])));
-          const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          if (mx > m) {
-            if (m > -INFINITY) {
-              const float dm = fmaxf(m - mx, floor_v), c = ex2(dm * c2);
-              t = c * fmaf(s, dm, t);
-              s *= c;
-            }
-            m = mx;
-          }
-          const float m0 = m > -INFINITY ? m : 0.0f;
-          float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f}, pt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float dz = max_nan(__uint_as_float(v[h][c]) - m0, floor_v);
-            const float e = ex2(dz * c2);
-            ps[c & 3] += e;
-            pt[c & 3] = fmaf(e, dz, pt[c & 3]);
-          }
-          s += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-          t += (pt[0] + pt[1]) + (pt[2] + pt[3]);
-          if (mx > limit) {
-            uint32_t hit = 0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              zs[c * 128 + r] = __uint_as_float(v[h][c]);
-              hit |= (uint32_t)(__uint_as_float(v[h][c]) > limit) << c;
-            }
-            while (hit) {
-              const int c = __ffs((int)hit) - 1;
-              hit &= hit - 1;
-              const float z = zs[c * 128 + r];
-              if (z > limit) {
-                mine = heap_keep(hv, hl, r, n, A.kp, z, (int32_t)(l0 + c));
-                n = min(n + 1, A.kp);
-                if (mine > limit) {
-                  limit = mine;
-                  atomicMax(A.tau + row, ord32(mine));
+                for (int k = 0; k < 4; ++k) {          // 32 bytes of K an instruction
+                  const uint64_t bd = sw128_desc(wk + k * 32, 16, 1024);
+                  const uint32_t more = (kb | op | k) != 0;
+                  if (kXs) {
+                    const uint64_t ad = sw128_desc(ws + wbytes + (uint32_t)(op * A.kbs + i) * 16384 + k * 32, 16, 1024);
+                    if (kFp8) mma_e4m3(dcol, ad, bd, idesc[op], more);
+                    else mma_bf16(dcol, ad, bd, idesc[0], more);
+                  } else {
+                    const uint32_t a = tmem + (uint32_t)op * opcols + (uint32_t)kb * 32 + (uint32_t)k * 8;
+                    if (kFp8) mma_e4m3_ts(dcol, a, bd, idesc[op], more);
+                    else mma_bf16_ts(dcol, a, bd, idesc[0], more);
+                  }
                 }
               }
             }
+            if (st == nst - 1) mma_commit(&S->tfull[buf]);
+          }
+          if (!ok) break;
+          mma_commit(&S->empty[s]);
+          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp < 10) {
+    const int par = (warp - 2) >> 2;                   // tiles of this parity (t0 is even)
+    const int quad = warp & 3, r = quad * 32 + lane, row = p * 128 + r;
+    const bool live = row < A.B;
+    const float inv = live ? A.xinv[row] : 1.0f;
+    Soft soft;
+    soft.c2 = inv * kLog2e;
+    soft.floor_v = kFloor / inv;
+    float* bm = A.bmax + ((size_t)row * 2 + par) * A.nblkp;
+    float win[8];                                      // maxima of the aligned eight blocks under way
+    uint32_t nt = 0;
+    bool ok = true;
+    for (int64_t blk = blk0; blk < blk1 && ok; ++blk) {
+      float best = -INFINITY;
+      for (int i = 0; i < A.pairs; ++i) {
+        const int64_t tile = 2 * (blk * A.pairs + i) + par;
+        if (tile >= t1) break;
+        if (!mbar_wait(&S->tfull[par], nt & 1, abort, kWait)) { record_timeout(A.status, abort, 74); ok = false; break; }
+        ++nt;
+        tc_fence_after();
+#pragma unroll 1
+        for (int u = 0; u < kN / 64; ++u) {
+          __syncwarp();
+          uint32_t v[2][32];
+          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (kXs ? 0 : kAccCol) + par * kN + u * 64;
+          tmem_ld32(at, v[0]);
+          tmem_ld32(at + 32, v[1]);
+          tmem_wait_ld();
+          if (u == kN / 64 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S->tempty[par]);
+          }
+          if (!live) continue;
+          const int64_t l0 = tile * kN + u * 64;
+          if (l0 + 64 > A.L) {                         // past the end there are no labels
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (l0 + c >= A.L) v[c >> 5][c & 31] = __float_as_uint(kNoLabel);
+            if (l0 >= A.L) continue;
+          }
+          best = fmaxf(best, soft.add32(v[0]));
+          if (l0 + 32 < A.L) best = fmaxf(best, soft.add32(v[1]));
+        }
+      }
+      if (A.k > 0 && live) {
+        const int j = (int)blk & 7;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) win[e] = e == j ? best : win[e];
+        if (j == 7 || blk + 1 == blk1) {
+          const int64_t first = blk - j;
+          if (j == 7 && first >= blk0) {
+            reinterpret_cast<float4*>(bm + first)[0] = make_float4(win[0], win[1], win[2], win[3]);
+            reinterpret_cast<float4*>(bm + first)[1] = make_float4(win[4], win[5], win[6], win[7]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e <= j && first + e >= blk0) bm[first + e] = win[e];
           }
         }
       }
     }
-    if (live) {
-      A.part[(size_t)row * A.G + g] = {m * inv, s, t * inv};
-      const size_t o = ((size_t)row * A.G + g) * A.kp;
-      for (int i = 0; i < A.kp; ++i) {
-        A.cand_v[o + i] = i < n ? hv[i * 128 + r] : 0.0f;
-        A.cand_i[o + i] = i < n ? hl[i * 128 + r] : -1;
-      }
-    }
+    if (live) A.part[(size_t)row * 2 * A.G + 2 * g + par] = {soft.m * inv, soft.s, soft.t * inv};
   } else if (scan) {
-    // magnitudes as whole numbers: 16 bits (bf16) or 8 (the bytes of each half in turn)
-    const int id = (warp - 6) * 32 + lane;
-    uint32_t mx = 0, it = 0;
-    for (int64_t t = t0; t < t1 && !*abort; ++t) {
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % (uint32_t)A.stages, ph = (it / (uint32_t)A.stages) & 1;
-        if (!mbar_wait(&S->full[s], ph, abort, kWait)) { record_timeout(A.status, abort, 75); break; }
-        const uint4* w = reinterpret_cast<const uint4*>(ring + (size_t)s * kStage);
-#pragma unroll 4
-        for (int i = id; i < (int)kWBytes / 16; i += 64) {
-          const uint4 v = w[i];
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    // bf16 magnitudes by 16-bit maxima, two instructions for two weights.  Of
+    // 8-bit magnitudes x, x + (0x7F - m) carries into the sign bit exactly
+    // where x exceeds the largest so far, m: two and a half for four, and m
+    // seldom moves.  Panels of one range take its stages in turn.
+    const int id = (warp - 10) * 32 + lane;
+    uint32_t mx = 0, s = 0, ph = 0, turn = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < t1 && ok && !*abort; t += A.q) {
+      for (int st = 0; st < nst; ++st) {
+        if (!mbar_wait(&S->full[s], ph, abort, kWait)) { record_timeout(A.status, abort, 75); ok = false; break; }
+        if (turn == (uint32_t)p) {
+          const uint4* w = reinterpret_cast<const uint4*>(ring + (size_t)s * stage);
+          for (uint32_t i = id; i < wbytes / 16; i += 64 * 8) {      // stages are multiples of 8 KB
+            uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (kFp8) {
-              mx = __vmaxu2(mx, x[e] & 0x7F007F00u);
-              mx = __vmaxu2(mx, (x[e] << 8) & 0x7F007F00u);
+            for (int e = 0; e < 8; ++e) v[e] = w[i + 64 * e];
+            if constexpr (!kFp8) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, v[e].x & 0x7FFF7FFFu), __vmaxu2(v[e].y & 0x7FFF7FFFu, v[e].z & 0x7FFF7FFFu)),
+                              v[e].w & 0x7FFF7FFFu);
             } else {
-              mx = __vmaxu2(mx, x[e] & 0x7FFF7FFFu);
+              const uint32_t add = 0x7F7F7F7Fu - mx * 0x01010101u;
+              uint32_t any = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                any |= ((v[e].x & 0x7F7F7F7Fu) + add) | ((v[e].y & 0x7F7F7F7Fu) + add) | ((v[e].z & 0x7F7F7F7Fu) + add) |
+                       ((v[e].w & 0x7F7F7F7Fu) + add);
+              if (__any_sync(0xFFFFFFFFu, any & 0x80808080u)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t x[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int h = 0; h < 32; h += 8) mx = max(mx, (x[c] >> h) & 0x7Fu);
+                }
+                mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+              }
             }
           }
         }
+        if (++turn == (uint32_t)P) turn = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S->empty[s]);
+        if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
       }
     }
-    mx = max(mx & 0xFFFFu, mx >> 16) >> (kFp8 ? 8 : 0);
-    for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if (lane == 0 && mx) atomicMax(A.wmax, mx);
+    if (!kFp8) mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
+    if (lane == 0 && mx) atomicMax(&A.counts->wmax, mx);
   }
   __syncthreads();
   if (*abort) __nanosleep(20000);                      // copies in flight land before the memory is given up
@@ -484,36 +566,75 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- exact scores
-// x . w_l with exact products and sums in 64 bits, by one warp, in an order
-// that depends on d alone: equal rows have equal scores.
-__device__ __forceinline__ double exact_score(const double* xs, const void* W, int fmt, int64_t l, int d, int lane) {
-  double acc = 0.0;
-  if (fmt == ELMO_BF16) {
-    const uint4* w = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + l * d);
-    for (int c = lane; c < d / 8; c += 32) {
-      const uint4 v = w[c];
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// Eight weights of a label from element 8 c on, as they are stored; kFormat is
+// the head's format, so that a loop's loads all start before the first is used.
+template <int kFormat> struct Raw8 { uint2 v; };
+template <> struct Raw8<ELMO_BF16> { uint4 v; };
+
+template <int kFormat>
+__device__ __forceinline__ Raw8<kFormat> load8(const void* W, int64_t l, int d, int c) {
+  Raw8<kFormat> r;
+  if constexpr (kFormat == ELMO_BF16) r.v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + l * d) + c);
+  else r.v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(W) + l * d) + c);
+  return r;
+}
+template <int kFormat>
+__device__ __forceinline__ void values8(const Raw8<kFormat>& r, float (&f)[8]) {
+  if constexpr (kFormat == ELMO_BF16) {
+    const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc = fma(xs[8 * c + 2 * e], (double)__uint_as_float(u[e] << 16), acc);
-        acc = fma(xs[8 * c + 2 * e + 1], (double)__uint_as_float(u[e] & 0xFFFF0000u), acc);
-      }
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(u[e] << 16);
+      f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
     }
   } else {
-    const uint2* w = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(W) + l * d);
-    for (int c = lane; c < d / 8; c += 32) {
-      const uint2 v = w[c];
-      float f[8];
-      float(&a)[4] = *reinterpret_cast<float(*)[4]>(f);
-      float(&b)[4] = *reinterpret_cast<float(*)[4]>(f + 4);
-      if (fmt == ELMO_FP8_E5M2) { e5m2x4_to_f32(v.x, a); e5m2x4_to_f32(v.y, b); }
-      else { e4m3x4_to_f32(v.x, a); e4m3x4_to_f32(v.y, b); }
+    float a[4], b[4];
+    if constexpr (kFormat == ELMO_FP8_E5M2) { e5m2x4_to_f32(r.v.x, a); e5m2x4_to_f32(r.v.y, b); }
+    else { e4m3x4_to_f32(r.v.x, a); e4m3x4_to_f32(r.v.y, b); }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fma(xs[8 * c + e], (double)f[e], acc);
-    }
+    for (int e = 0; e < 4; ++e) { f[e] = a[e]; f[4 + e] = b[e]; }
+  }
+}
+
+// x . w_l with exact products and sums in 64 bits, by one warp, in an order
+// that depends on d alone: equal rows have equal scores.
+template <int kFormat>
+__device__ __forceinline__ double exact_score(const float* xs, const void* W, int64_t l, int d, int lane) {
+  double acc = 0.0;
+#pragma unroll 4
+  for (int c = lane; c < d / 8; c += 32) {
+    float f[8];
+    values8<kFormat>(load8<kFormat>(W, l, d, c), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc = fma((double)xs[8 * c + e], (double)f[e], acc);
   }
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
   return acc;
+}
+
+// The same in fp32 for kM labels at a time.
+template <int kFormat, int kM>
+__device__ __forceinline__ void near_scores(const uint16_t* X, const void* W, const int64_t (&l)[kM], int d, int lane,
+                                            float (&acc)[kM]) {
+#pragma unroll
+  for (int m = 0; m < kM; ++m) acc[m] = 0.0f;
+  for (int c = lane; c < d / 8; c += 32) {
+    Raw8<kFormat> r[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) r[m] = load8<kFormat>(W, l[m], d, c);
+    float x[8];
+    values8<ELMO_BF16>(load8<ELMO_BF16>(X, 0, d, c), x);
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      float f[8];
+      values8<kFormat>(r[m], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[m] = fmaf(x[e], f[e], acc[m]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
 }
 
 __device__ __forceinline__ float max_weight(uint32_t code, int fmt) {
@@ -523,37 +644,93 @@ __device__ __forceinline__ float max_weight(uint32_t code, int fmt) {
 }
 
 // ---------------------------------------------------------------- 3. join
+struct SmemB {
+  float gbest[kGroups];
+  float low;
+};
+
+// low = a lower bound on the k-th best of values of which each thread has seen
+// the best of its own: the k-th best of the groups of kPer neighbouring
+// threads (-inf where fewer groups hold a value).
+template <int kThr>
+__device__ __forceinline__ float lower_bound_kth(SmemB* S, float best, int k) {
+  constexpr int kPer = kThr / kGroups;
+  const int tid = threadIdx.x;
+  for (int o = 1; o < kPer; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  __syncthreads();
+  if (tid % kPer == 0) S->gbest[tid / kPer] = best;
+  if (tid == 0) S->low = -INFINITY;
+  __syncthreads();
+  if (tid < kGroups) {
+    const float mine = S->gbest[tid];
+    int above = 0, same = 0;
+    for (int j = 0; j < kGroups; ++j) { above += S->gbest[j] > mine; same += S->gbest[j] == mine; }
+    if (above < k && above + same >= k) S->low = mine;
+  }
+  __syncthreads();
+  return S->low;
+}
+
+// 2 delta of a query, rounded up; 2^-126 for subnormal partial sums
+__device__ __forceinline__ float two_delta(const Args& A, int b) {
+  float d = __fmul_ru(A.gamma, __fadd_ru(A.n1[b], A.r1[b]));
+  d = __fmul_ru(__fadd_ru(d, A.r1[b]), max_weight(A.counts->wmax, A.fmt));
+  return __fmul_ru(2.0f, __fadd_ru(d, 0x1p-126f));
+}
+
+// Statistics of a query, log p of its given labels, and the blocks that may
+// hold its k best labels.
+template <int kFormat>
 __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) {
-  extern __shared__ double dyn[];
-  double* xs = dyn;                                    // [d] the query
-  __shared__ double ex[kMaxCand];                      // exact scores of the ones ranked
-  __shared__ float cv[kMaxCand];                       // kept scores near the best
-  __shared__ int32_t ci[kMaxCand];
-  __shared__ double stat[2];
-  __shared__ int count;
-  __shared__ float kth, low;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  float* xs = reinterpret_cast<float*>(dyn);           // [d] the query
+  __shared__ SmemB S;
+  __shared__ int32_t blocks[kMaxBlocks];
   constexpr int kW = kJoinThreads / 32;
+  __shared__ double stat[2], ws[kW], wt[kW];
+  __shared__ float wm[kW];
+  __shared__ int nblocks, at0;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int j = tid; j < A.d / 2; j += kJoinThreads) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(A.X + (size_t)b * A.d)[j];
+    xs[2 * j] = __uint_as_float(w << 16);
+    xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+  if (tid == 0) nblocks = 0;
+  pdl_wait();
   const bool bad = A.rflag[b] != 0;
-  for (int j = tid; j < A.d; j += kJoinThreads) xs[j] = (double)bf16_to_f32(A.X[(size_t)b * A.d + j]);
-  if (warp == 0) {
-    const Stat* part = A.part + (size_t)b * A.G;
+  {
+    // at most two partial sums of a thread: 2 G <= 2 SMs
+    const int n = 2 * A.G;
+    const Stat* part = A.part + (size_t)b * n;
+    Stat q[2];
     float mf = -INFINITY;
-    for (int i = lane; i < A.G; i += 32) mf = fmaxf(mf, part[i].m);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q[i] = tid + i * kJoinThreads < n ? part[tid + i * kJoinThreads] : Stat{-INFINITY, 0.0f, 0.0f};
+      mf = fmaxf(mf, q[i].m);
+    }
     for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xFFFFFFFFu, mf, o));
+    if (lane == 0) wm[warp] = mf;
+    __syncthreads();
+    for (int w = 0; w < kW; ++w) mf = fmaxf(mf, wm[w]);
     double s = 0.0, t = 0.0;
-    for (int i = lane; i < A.G; i += 32) {
-      const Stat q = part[i];
-      if (q.m == -INFINITY) { s += q.s; continue; }
-      const double d = (double)q.m - (double)mf, c = q.m == mf ? 1.0 : exp(d);
-      s += c * q.s;
-      t += c * (q.t + (q.m == mf ? 0.0 : d * q.s));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (q[i].m == -INFINITY) { s += q[i].s; continue; }
+      const double d = (double)q[i].m - (double)mf, c = q[i].m == mf ? 1.0 : exp(d);
+      s += c * q[i].s;
+      t += c * (q[i].t + (q[i].m == mf ? 0.0 : d * q[i].s));
     }
     for (int o = 16; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
       t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
-    if (lane == 0) {
+    if (lane == 0) { ws[warp] = s; wt[warp] = t; }
+    __syncthreads();
+    if (tid == 0) {
+      s = t = 0.0;
+      for (int w = 0; w < kW; ++w) { s += ws[w]; t += wt[w]; }
       double m = mf, logs = log(s), lse = m + logs, H = logs - t / s;
       if (mf == -INFINITY) {                           // no label has a finite score
         lse = s == 0.0 ? -INFINITY : NAN;
@@ -573,9 +750,69 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
       A.rowstat[2 * b + 1] = logs;
     }
   }
-  if (tid == 0) count = 0;
   __syncthreads();
   const double m = stat[0], logs = stat[1];
+
+  if (A.k > 0) {
+    if (bad) {
+      if (tid == 0) A.listed[b] = 0;
+      for (int i = tid; i < A.k; i += kJoinThreads) {
+        A.top_idx[(size_t)b * A.k + i] = -1;
+        A.top_logp[(size_t)b * A.k + i] = -INFINITY;
+      }
+    } else {
+      const float two = two_delta(A, b), inv = A.xinv[b];
+      bool ok = two < INFINITY;                        // not so for weights that are not finite
+      const float4* bm = reinterpret_cast<const float4*>(A.bmax + (size_t)b * 2 * A.nblkp);
+      const int n4 = A.nblkp / 2;                      // vectors of both parities
+      // entry e of vector i is block (4 i + e) mod nblkp of parity 4 i >= nblkp
+      auto count_of = [&](int i) { return min(4, A.nblk - (4 * i < A.nblkp ? 4 * i : 4 * i - A.nblkp)); };
+      auto each = [&](auto f) {
+        for (int i0 = tid; i0 < n4; i0 += 8 * kJoinThreads) {
+          float4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (i0 + u * kJoinThreads < n4) v[u] = __ldcg(bm + i0 + u * kJoinThreads);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kJoinThreads;
+            if (i >= n4) break;
+            const int c = count_of(i);
+            if (c > 0) f(i, 0, v[u].x);
+            if (c > 1) f(i, 1, v[u].y);
+            if (c > 2) f(i, 2, v[u].z);
+            if (c > 3) f(i, 3, v[u].w);
+          }
+        }
+      };
+      float best = -INFINITY;
+      if (ok) each([&](int, int, float v) { best = fmaxf(best, v); });
+      const float low = lower_bound_kth<kJoinThreads>(&S, best, A.k);
+      const float from = __fsub_rd(low, __fdiv_ru(two, inv));
+      if (ok)
+        each([&](int i, int e, float v) {
+          if (v >= from && v > -INFINITY) {
+            const int at = atomicAdd(&nblocks, 1);
+            if (at < kMaxBlocks) blocks[at] = 4 * i + e;
+          }
+        });
+      __syncthreads();
+      const int n = nblocks;
+      ok = ok && n > 0 && n <= kMaxBlocks;
+      if (tid == 0) {
+        A.listed[b] = ok;
+        if (ok) {
+          at0 = atomicAdd(&A.counts->nitems, n);
+          A.from[b] = __fsub_rd(__fmul_rd(low, inv), two);
+        } else {
+          A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
+        }
+      }
+      __syncthreads();
+      if (ok)
+        for (int i = tid; i < n; i += kJoinThreads) A.items[at0 + i] = make_int2(b, blocks[i]);
+    }
+  }
 
   const int e0 = max(A.rowptr[b], 0), e1 = min(A.rowptr[b + 1], A.nnz);
   for (int e = e0 + warp; e < e1; e += kW) {
@@ -586,87 +823,101 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     } else if (l < 0 || l >= A.L) {
       r = -INFINITY;                                   // another device's label
     } else {
-      const double z = exact_score(xs, A.W, A.fmt, l, A.d, lane);
+      const double z = exact_score<kFormat>(xs, A.W, l, A.d, lane);
       r = z == -INFINITY && !isnan(m + logs) ? -INFINITY : (float)(z - m - logs);
     }
     if (lane == 0) A.logp[e] = r;
   }
+}
 
-  if (A.k == 0) return;
-  if (bad) {
-    for (int i = tid; i < A.k; i += kJoinThreads) {
-      A.top_idx[(size_t)b * A.k + i] = -1;
-      A.top_logp[(size_t)b * A.k + i] = -INFINITY;
-    }
-    return;
-  }
-  const uint32_t tau_key = A.tau[b];
-  const float tau = ord32_value(tau_key);
-  const size_t base = (size_t)b * A.G * A.kp;
-  const int nc = A.G * A.kp;
-  const float inv = A.xinv[b];
-  // 2 delta in the accumulators' units, rounded up; 2^-126 for subnormal partial sums
-  float delta = __fmul_ru(A.gamma, __fadd_ru(A.n1[b], A.r1[b]));
-  delta = __fmul_ru(__fadd_ru(delta, A.r1[b]), max_weight(*A.wmax, A.fmt));
-  const float two = __fdiv_ru(__fmul_ru(2.0f, __fadd_ru(delta, 0x1p-126f)), inv);
-  // of the ranges' lists, only what comes within 2 delta of the k-th best: the
-  // k-th best of kGroups groups' best is at most that
-  float best = -INFINITY;
-  for (int i = tid; i < nc; i += kJoinThreads)
-    if (A.cand_i[base + i] >= 0) best = fmaxf(best, A.cand_v[base + i]);
-  for (int o = 1; o < kJoinThreads / kGroups; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-  if (tid % (kJoinThreads / kGroups) == 0) cv[tid / (kJoinThreads / kGroups)] = best;
-  if (tid == 0) low = -INFINITY;
-  __syncthreads();
-  if (tid < kGroups) {
-    const float mine = cv[tid];
-    int above = 0, same = 0;
-    for (int j = 0; j < kGroups; ++j) { above += cv[j] > mine; same += cv[j] == mine; }
-    if (above < A.k && above + same >= A.k) low = mine;
-  }
-  __syncthreads();
-  const float from = __fsub_rd(low, two);
-  for (int i = tid; i < nc; i += kJoinThreads) {
-    const int32_t l = A.cand_i[base + i];
-    if (l < 0) continue;
-    const float v = A.cand_v[base + i];
-    if (v >= from || !(two < INFINITY)) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kMaxCand) { cv[at] = v; ci[at] = l; }
+// The labels of the listed blocks again, in fp32, kNearAt of a block to a
+// warp.  Bound by the read of the blocks where there are many (256 queries'
+// 64 best among 3M 8-bit labels: 0.9 GB), by latency else: every load of a
+// step starts before the first is used, and the query comes from L1.
+template <int kFormat>
+__global__ void __launch_bounds__(kNearThreads) label_near_kernel(const Args A, int tile) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const int per = A.pairs * tile / kNearAt;
+  const int64_t work = (int64_t)A.counts->nitems * per;
+  for (int64_t w = (int64_t)blockIdx.x * (kNearThreads / 32) + (threadIdx.x >> 5); w < work;
+       w += (int64_t)gridDim.x * (kNearThreads / 32)) {
+    const int2 it = A.items[w / per];
+    const int b = it.x, in = (int)(w % per) * kNearAt;
+    const bool odd = it.y >= A.nblkp;
+    const int64_t pair0 = (int64_t)(odd ? it.y - A.nblkp : it.y) * A.pairs;
+    const int64_t l0 = (2 * (pair0 + in / tile) + odd) * tile + in % tile;
+    if (l0 >= A.L) continue;
+    int64_t l[kNearAt];
+    float z[kNearAt];
+#pragma unroll
+    for (int c = 0; c < kNearAt; ++c) l[c] = min(l0 + c, A.L - 1);
+    near_scores<kFormat, kNearAt>(A.X + (size_t)b * A.d, A.W, l, A.d, lane, z);
+    float mine = z[0];
+#pragma unroll
+    for (int c = 1; c < kNearAt; ++c) mine = lane == c ? z[c] : mine;
+    if (lane < kNearAt && l0 + lane < A.L && mine >= A.from[b]) {
+      const int at = atomicAdd(A.nnear + b, 1);
+      if (at < kMaxNear) {
+        A.near_v[(size_t)b * kMaxNear + at] = mine;
+        A.near_l[(size_t)b * kMaxNear + at] = (int32_t)(l0 + lane);
+      }
     }
   }
-  if (tid == 0) kth = -INFINITY;
-  __syncthreads();
-  const int n = count;
-  bool ok = n >= A.k && n <= kMaxCand;
+}
+
+// A query's k best of the labels near the k-th best, by exact scores.
+template <int kFormat>
+__global__ void __launch_bounds__(kNearThreads) label_rank_kernel(const Args A) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  float* xs = reinterpret_cast<float*>(dyn);           // [d]
+  __shared__ SmemB S;
+  __shared__ double ex[kMaxExact];
+  __shared__ int32_t el[kMaxExact];
+  __shared__ int nexact;
+  constexpr int kW = kNearThreads / 32;
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int j = tid; j < A.d / 2; j += kNearThreads) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(A.X + (size_t)b * A.d)[j];
+    xs[2 * j] = __uint_as_float(w << 16);
+    xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+  if (tid == 0) nexact = 0;
+  pdl_wait();
+  if (A.listed[b] == 0) return;                          // answered, or a failed query already
+  const int near = A.nnear[b];
+  bool ok = near >= A.k && near <= kMaxNear;
+  const float* nv = A.near_v + (size_t)b * kMaxNear;
   if (ok) {
-    for (int i = tid; i < n; i += kJoinThreads) {      // the k-th best kept score, ties in any order
-      const float v = cv[i];
-      int above = 0, same = 0;
-      for (int j = 0; j < n; ++j) { above += cv[j] > v; same += cv[j] == v; }
-      if (above < A.k && above + same >= A.k) kth = v;
+    const float two = two_delta(A, b);
+    float best = -INFINITY;
+    for (int i = tid; i < near; i += kNearThreads) best = fmaxf(best, nv[i]);
+    const float cut = __fsub_rd(lower_bound_kth<kNearThreads>(&S, best, A.k), two);
+    for (int i = tid; i < near; i += kNearThreads) {
+      if (nv[i] >= cut) {
+        const int at = atomicAdd(&nexact, 1);
+        if (at < kMaxExact) el[at] = A.near_l[(size_t)b * kMaxNear + i];
+      }
     }
+    __syncthreads();
+    ok = nexact <= kMaxExact;
   }
-  __syncthreads();
-  const float cut = __fsub_rd(kth, two);
-  ok = ok && (tau_key == 0 || cut > tau) && two < INFINITY;           // NaN (weights that are not finite) fails too
   if (!ok) {
-    if (tid == 0) A.fail[atomicAdd(A.nfail, 1)] = b;
+    if (tid == 0) A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
     return;
   }
+  const int n = nexact;
   for (int i = warp; i < n; i += kW) {
-    double z = 0.0;
-    const bool in = cv[i] >= cut;
-    if (in) z = exact_score(xs, A.W, A.fmt, ci[i], A.d, lane);
-    if (lane == 0) ex[i] = in ? z : -INFINITY;
+    const double z = exact_score<kFormat>(xs, A.W, el[i], A.d, lane);
+    if (lane == 0) ex[i] = z;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kJoinThreads) {
-    if (!(cv[i] >= cut)) continue;
+  const double m = A.rowstat[2 * b], logs = A.rowstat[2 * b + 1];
+  for (int i = tid; i < n; i += kNearThreads) {
     const double z = ex[i];
-    const int32_t l = ci[i];
+    const int32_t l = el[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += ex[j] > z || (ex[j] == z && ci[j] < l);
+    for (int j = 0; j < n; ++j) rank += ex[j] > z || (ex[j] == z && el[j] < l);
     if (rank < A.k) {
       A.top_idx[(size_t)b * A.k + rank] = (int32_t)(l + A.label_base);
       A.top_logp[(size_t)b * A.k + rank] = (float)(z - m - logs);
@@ -706,30 +957,34 @@ __device__ __forceinline__ void best_after(int n, F at, uint64_t last_k, int32_t
     if (ranks_before(rk[w], ri[w], key, idx)) { key = rk[w]; idx = ri[w]; }
 }
 
-// Work item (failed row, segment): the segment's k best labels.
+// Work item (failed query, segment): the segment's k best labels; the CTA that
+// does a query's last segment joins them.
+template <int kFormat>
 __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A) {
-  extern __shared__ double dyn[];
-  double* xs = dyn;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  float* xs = reinterpret_cast<float*>(dyn);
   __shared__ uint64_t key[kExactChunk + ELMO_MAX_TOPK];
   __shared__ uint64_t lk[ELMO_MAX_TOPK];
   __shared__ int32_t li[ELMO_MAX_TOPK];
   __shared__ int32_t old[ELMO_MAX_TOPK];
   __shared__ uint64_t rk[kExactThreads / 32];
   __shared__ int32_t ri[kExactThreads / 32];
+  __shared__ int last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nf = *A.nfail;
+  pdl_wait();
+  const int nf = A.counts->nfail;
   for (int64_t item = blockIdx.x; item < (int64_t)nf * kSegs; item += gridDim.x) {
     const int r = (int)(item / kSegs), seg = (int)(item % kSegs);
     const int b = A.fail[r];
     const int64_t l0 = A.L * seg / kSegs, l1 = A.L * (seg + 1) / kSegs;
     __syncthreads();
-    for (int j = tid; j < A.d; j += kExactThreads) xs[j] = (double)bf16_to_f32(A.X[(size_t)b * A.d + j]);
+    for (int j = tid; j < A.d; j += kExactThreads) xs[j] = bf16_to_f32(A.X[(size_t)b * A.d + j]);
     if (tid < A.k) { lk[tid] = 0; li[tid] = 0x7FFFFFFF; }
     __syncthreads();
     for (int64_t a = l0; a < l1; a += kExactChunk) {
       const int n = (int)min((int64_t)kExactChunk, l1 - a);
       for (int i = warp; i < n; i += kExactThreads / 32) {
-        const double z = exact_score(xs, A.W, A.fmt, a + i, A.d, lane);
+        const double z = exact_score<kFormat>(xs, A.W, a + i, A.d, lane);
         if (lane == 0) key[i] = ord64(z);
       }
       if (tid < A.k) { key[kExactChunk + tid] = lk[tid]; old[tid] = li[tid]; }
@@ -754,60 +1009,62 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
       }
       __syncthreads();
     }
+    uint64_t* sk = A.seg_key + (size_t)r * kSegs * A.k;
+    int32_t* si = A.seg_i + (size_t)r * kSegs * A.k;
     if (tid < A.k) {
-      A.seg_key[((size_t)r * kSegs + seg) * A.k + tid] = lk[tid];
-      A.seg_i[((size_t)r * kSegs + seg) * A.k + tid] = li[tid];
+      __stcg(reinterpret_cast<unsigned long long*>(sk) + seg * A.k + tid, (unsigned long long)lk[tid]);
+      __stcg(si + seg * A.k + tid, li[tid]);
     }
-  }
-}
-
-__global__ void __launch_bounds__(kExactThreads) label_exact_join_kernel(const Args A) {
-  __shared__ uint64_t rk[kExactThreads / 32];
-  __shared__ int32_t ri[kExactThreads / 32];
-  const int nf = *A.nfail;
-  for (int r = blockIdx.x; r < nf; r += gridDim.x) {
-    const int b = A.fail[r];
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) last = atomicAdd(A.done + r, 1) == kSegs - 1;
+    __syncthreads();
+    if (!last) continue;
+    __threadfence();
     const double m = A.rowstat[2 * b], logs = A.rowstat[2 * b + 1];
-    const uint64_t* sk = A.seg_key + (size_t)r * kSegs * A.k;
-    const int32_t* si = A.seg_i + (size_t)r * kSegs * A.k;
-    auto at = [&](int i, uint64_t& k, int32_t& l) { k = sk[i]; l = si[i]; };
+    auto at = [&](int i, uint64_t& k, int32_t& l) {
+      k = __ldcg(reinterpret_cast<const unsigned long long*>(sk) + i);
+      l = __ldcg(si + i);
+    };
     uint64_t pk = ~0ull;
     int32_t pi = -1;
     for (int q = 0; q < A.k; ++q) {
       uint64_t k = 0;
       int32_t l = 0;
       if (pk != 0) best_after(kSegs * A.k, at, pk, pi, rk, ri, k, l);
-      if (threadIdx.x == 0) {
+      if (tid == 0) {
         A.top_idx[(size_t)b * A.k + q] = k ? (int32_t)(l + A.label_base) : -1;
         A.top_logp[(size_t)b * A.k + q] = k ? (float)(ord64_value(k) - m - logs) : -INFINITY;
       }
       pk = k;
       pi = l;
     }
-    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- host
 struct Layout {
-  int G, kp;
-  size_t xa, xb, xinv, n1, r1, rflag, wmax, nfail, fail, tau, cv, ci, part, sk, si, rowstat, total;
+  int G, nblk, nblkp, pairs;
+  size_t xa, xb, xinv, n1, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
+      rowstat, total;
 };
 
-// Scores kept beyond k: enough that the k-th best clears the kp-th by more
-// than 2 delta on ordinary rows.
-int kept(int k) { return k == 0 ? 0 : (k + 11 + k / 12 + 7) / 8 * 8; }
+int tile_labels(const elmo_head* h) { return h->d <= 768 ? 64 : 128; }
 
 Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   Layout o{};
   const bool fp8 = h->dt != ELMO_BF16;
   const int P = (B + 127) / 128;
-  const int64_t N = h->d <= 768 ? 64 : 128, T = (h->L + N - 1) / N;
+  const int64_t N = tile_labels(h), T = (h->L + N - 1) / N;
+  o.pairs = 1;
+  if (k > 0)
+    while ((size_t)B * (T / o.pairs) * 4 > kMaxima) o.pairs *= 2;
+  o.nblk = (int)((T + 2 * o.pairs - 1) / (2 * o.pairs));
+  o.nblkp = (o.nblk + 7) / 8 * 8;
   int64_t G = h->num_sms / P;
-  if (G > T) G = T;
+  if (G > o.nblk) G = o.nblk;
   if (G < 1) G = 1;
   o.G = (int)G;
-  o.kp = kept(k);
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += (bytes + 255) / 256 * 256; return at; };
   o.xa = take(fp8 ? (size_t)B * h->d : 0);
@@ -816,13 +1073,18 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   o.n1 = take(4 * (size_t)B);
   o.r1 = take(4 * (size_t)B);
   o.rflag = take(4 * (size_t)B);
-  o.wmax = take(4);
-  o.nfail = take(4);
-  o.fail = take(4 * (size_t)B);
-  o.tau = take(4 * (size_t)B);
-  o.cv = take(4 * (size_t)B * o.G * o.kp);
-  o.ci = take(4 * (size_t)B * o.G * o.kp);
-  o.part = take(sizeof(Stat) * (size_t)B * o.G);
+  o.counts = take(sizeof(Counts));
+  const size_t lists = k > 0 ? (size_t)B : 0;
+  o.fail = take(4 * lists);
+  o.done = take(4 * lists);
+  o.items = take(sizeof(int2) * lists * kMaxBlocks);
+  o.listed = take(4 * lists);
+  o.nnear = take(4 * lists);
+  o.near_v = take(4 * lists * kMaxNear);
+  o.near_l = take(4 * lists * kMaxNear);
+  o.from = take(4 * lists);
+  o.bmax = take(k > 0 ? 8 * (size_t)B * o.nblkp : 0);
+  o.part = take(sizeof(Stat) * (size_t)B * 2 * o.G);
   o.sk = take(8 * (size_t)B * kSegs * k);
   o.si = take(4 * (size_t)B * kSegs * k);
   o.rowstat = take(16 * (size_t)B);
@@ -834,27 +1096,48 @@ template <int kFp8, int kW5, int kXs>
 cudaError_t run_pass(elmo_head* h, Args A, cudaStream_t s) {
   constexpr int kN = kXs ? 128 : 64;
   constexpr int kOps = kFp8 ? 2 : 1;
-  constexpr size_t kStage = kN * 128 + (kXs ? 16384 * kOps : 0);
-  const size_t fixed = 1024 + 4 * 32 * 128 + (size_t)A.kp * 128 * 8 + sizeof(SmemP);
-  int stages = (int)((kSmemMost - fixed) / kStage);
-  if (stages > kMaxStages) stages = kMaxStages;
-  A.stages = stages;
   const int eb = kFp8 ? 1 : 2;
+  const int nkb = (A.d * eb + 127) / 128;
+  // up to 48 KB of W a stage (32 KB beside X), boxes of at most 256 labels
+  A.kbs = kXs ? 2 : (nkb + (nkb + 5) / 6 - 1) / ((nkb + 5) / 6);
+  A.q = kXs ? 1 : 6 / A.kbs < 4 ? 6 / A.kbs : 4;
+  if (nkb > A.kbs) A.q = 1;
+  A.kb3d = A.d * eb % 128 == 0;
+  const size_t stage = (size_t)A.kbs * (A.q * kN * 128 + (kXs ? 16384 * kOps : 0));
+  const size_t fixed = 1024 + sizeof(SmemP);
+  int stages = (int)((kSmemMost - fixed) / stage);
+  A.stages = stages < kMaxStages ? stages : kMaxStages;
   CUtensorMap tmW, tmA, tmB;
-  cudaError_t e = make_tma_map_2d(&tmW, h->W, eb, (uint64_t)h->d, (uint64_t)h->L, (uint64_t)h->d, kN);
+  auto map = [&](CUtensorMap* m, const void* p, int64_t rows, int box) {
+    return A.kb3d ? make_tma_map_kb3d(m, p, eb, (uint64_t)A.d, (uint64_t)rows, (uint32_t)box, (uint32_t)A.kbs)
+                  : make_tma_map_2d(m, p, eb, (uint64_t)A.d, (uint64_t)rows, (uint64_t)A.d, (uint32_t)box);
+  };
+  cudaError_t e = map(&tmW, h->W, h->L, A.q * kN);
   if (e != cudaSuccess) return e;
   tmA = tmB = tmW;
   if (kXs) {
-    const void* a = kFp8 ? static_cast<const void*>(A.xa) : A.X;
-    if ((e = make_tma_map_2d(&tmA, a, eb, (uint64_t)h->d, (uint64_t)A.B, (uint64_t)h->d, 128)) != cudaSuccess) return e;
-    if (kFp8 && (e = make_tma_map_2d(&tmB, A.xb, eb, (uint64_t)h->d, (uint64_t)A.B, (uint64_t)h->d, 128)) != cudaSuccess)
-      return e;
+    if ((e = map(&tmA, kFp8 ? static_cast<const void*>(A.xa) : A.X, A.B, 128)) != cudaSuccess) return e;
+    if (kFp8 && (e = map(&tmB, A.xb, A.B, 128)) != cudaSuccess) return e;
   }
   auto kern = label_score_kernel<kFp8, kW5, kXs>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
   if (e != cudaSuccess) return e;
   const int P = (A.B + 127) / 128;
-  kern<<<P * A.G, kThreads, fixed + stages * kStage, s>>>(tmW, tmA, tmB, A);
+  kern<<<P * A.G, kThreads, fixed + A.stages * stage, s>>>(tmW, tmA, tmB, A);
+  return cudaGetLastError();
+}
+
+template <int kFormat>
+cudaError_t run_join(elmo_head* h, const Args& A, cudaStream_t s) {
+  const size_t xbytes = sizeof(float) * (size_t)h->d;
+  label_join_kernel<kFormat><<<A.B, kJoinThreads, xbytes, s>>>(A);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || A.k == 0) return e;
+  label_near_kernel<kFormat><<<h->num_sms * 4, kNearThreads, 0, s>>>(A, tile_labels(h));
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  label_rank_kernel<kFormat><<<A.B, kNearThreads, xbytes, s>>>(A);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  label_exact_kernel<kFormat><<<h->num_sms * 2, kExactThreads, xbytes, s>>>(A);
   return cudaGetLastError();
 }
 
@@ -877,7 +1160,8 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.L = h->L;
   A.label_base = h->label_base;
   A.labels_total = h->labels_total;
-  A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.kp = o.kp; A.nnz = nnz;
+  A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.nnz = nnz;
+  A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs;
   A.fmt = w_format(h);
   const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
   A.gamma = (float)nsteps * 0x1p-22f;
@@ -885,12 +1169,16 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.n1 = reinterpret_cast<float*>(ws + o.n1);
   A.r1 = reinterpret_cast<float*>(ws + o.r1);
   A.rflag = reinterpret_cast<int32_t*>(ws + o.rflag);
-  A.wmax = reinterpret_cast<uint32_t*>(ws + o.wmax);
-  A.nfail = reinterpret_cast<int32_t*>(ws + o.nfail);
+  A.counts = reinterpret_cast<Counts*>(ws + o.counts);
   A.fail = reinterpret_cast<int32_t*>(ws + o.fail);
-  A.tau = reinterpret_cast<uint32_t*>(ws + o.tau);
-  A.cand_v = reinterpret_cast<float*>(ws + o.cv);
-  A.cand_i = reinterpret_cast<int32_t*>(ws + o.ci);
+  A.done = reinterpret_cast<int32_t*>(ws + o.done);
+  A.items = reinterpret_cast<int2*>(ws + o.items);
+  A.listed = reinterpret_cast<int32_t*>(ws + o.listed);
+  A.nnear = reinterpret_cast<int32_t*>(ws + o.nnear);
+  A.near_v = reinterpret_cast<float*>(ws + o.near_v);
+  A.near_l = reinterpret_cast<int32_t*>(ws + o.near_l);
+  A.from = reinterpret_cast<float*>(ws + o.from);
+  A.bmax = reinterpret_cast<float*>(ws + o.bmax);
   A.part = reinterpret_cast<Stat*>(ws + o.part);
   A.seg_key = reinterpret_cast<uint64_t*>(ws + o.sk);
   A.seg_i = reinterpret_cast<int32_t*>(ws + o.si);
@@ -912,18 +1200,10 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
     else e = wide ? run_pass<1, 0, 1>(h, A, s) : run_pass<1, 0, 0>(h, A, s);
     if (e != cudaSuccess) return e;
   }
-  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k > 0 ? 3 : 1);
-  const size_t xbytes = sizeof(double) * (size_t)h->d;
-  e = cudaFuncSetAttribute(label_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 8);
-  if (e != cudaSuccess) return e;
-  label_join_kernel<<<B, kJoinThreads, xbytes, s>>>(A);
-  if ((e = cudaGetLastError()) != cudaSuccess || k == 0) return e;
-  e = cudaFuncSetAttribute(label_exact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4096 * 8);
-  if (e != cudaSuccess) return e;
-  label_exact_kernel<<<h->num_sms * 2, kExactThreads, xbytes, s>>>(A);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  label_exact_join_kernel<<<B < h->num_sms ? B : h->num_sms, kExactThreads, 0, s>>>(A);
-  return cudaGetLastError();
+  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k > 0 ? 4 : 1);
+  if (A.fmt == ELMO_BF16) return run_join<ELMO_BF16>(h, A, s);
+  if (A.fmt == ELMO_FP8_E5M2) return run_join<ELMO_FP8_E5M2>(h, A, s);
+  return run_join<ELMO_FP8_E4M3>(h, A, s);
 }
 
 }  // namespace elmo
