@@ -72,6 +72,8 @@ def library_path() -> str:
 def load():
     """Load libelmo.so (built in-tree by __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -138,7 +140,7 @@ def _check(rc: int):
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -156,33 +158,31 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _here(*tensors):
-    """Checks that the tensors live on the current device, whose stream the call uses."""
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _shape(name, t, shape, *dtypes):
-    """Checks a tensor's shape and element type (its layout where the call takes it dense is _ptr's)."""
+def _arg(name, t, shape, dtypes, pitch=False):
+    """The device address of an argument of the scoring calls, checked: its shape and element type, that it is dense
+    (pitch: its rows are) and lives on the current device, whose stream the call uses."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-
-
-def _rows_ptr(name, t):
-    """(pointer, row pitch in elements) of a 2-D tensor whose rows are dense."""
     if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be adjacent")
-    pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if pitch < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap")
-    return ctypes.c_void_p(t.data_ptr()), pitch
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if pitch:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be adjacent")
+        if _pitch(t) < t.shape[1]:
+            raise ValueError(f"{name}: rows overlap")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _pitch(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _dt(dtype) -> int:
@@ -360,18 +360,20 @@ def elmo_precision_at_k(idx: torch.Tensor, rowptr: torch.Tensor, cols: torch.Ten
 
 _BF16_BITS = (torch.bfloat16, torch.int16)
 _FP8_CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+_SCORE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 def _q4_copy(codes, scales):
-    """(L, d, group) of a 4-bit copy."""
+    """(address of the codes, of the scales, L, d, group) of a 4-bit copy."""
     if codes.dim() != 2 or scales.dim() != 2 or scales.shape[1] < 1:
         raise ValueError("codes must be [L, d / 2] and scales [L, d / group]")
-    L, d = codes.shape[0], 2 * codes.shape[1]
-    _shape("codes", codes, (L, d // 2), torch.uint8)
-    _shape("scales", scales, (L, scales.shape[1]), *_BF16_BITS)
-    if d % scales.shape[1]:
-        raise ValueError(f"{scales.shape[1]} scales a row do not divide d = {d}")
-    return L, d, d // scales.shape[1]
+    L, d, n = codes.shape[0], 2 * codes.shape[1], scales.shape[1]
+    if d % n:
+        raise ValueError(f"{n} scales a row do not divide d = {d}")
+    return _arg("codes", codes, (L, d // 2), _U8), _arg("scales", scales, (L, n), _BF16_BITS), L, d, d // n
 
 
 def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales: torch.Tensor, stream=None):
@@ -379,54 +381,42 @@ def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales
     byte with the even element low, and scales bf16 [L, d / group]; see include/elmo.h."""
     dt = _dt(dtype)
     L, d = W.shape
-    _shape("W", W, (L, d), *(_BF16_BITS if dt == BF16 else _FP8_CODES))
-    _shape("codes", codes, (L, d // 2), torch.uint8)
-    _shape("scales", scales, (L, d // int(group) if group > 0 else 0), *_BF16_BITS)
-    _here(W, codes, scales)
-    _check(load().elmo_q4_pack(_ptr(W), L, d, dt, int(group), _ptr(codes), _ptr(scales), _stream(stream)))
+    group = int(group)
+    _check(load().elmo_q4_pack(_arg("W", W, (L, d), _BF16_BITS if dt == BF16 else _FP8_CODES), L, d, dt, group,
+                               _arg("codes", codes, (L, d // 2), _U8),
+                               _arg("scales", scales, (L, d // group if group > 0 else 0), _BF16_BITS),
+                               _stream(stream)))
 
 
 def elmo_q4_unpack(codes: torch.Tensor, scales: torch.Tensor, W: torch.Tensor, stream=None):
     """W (bf16 [L, d]) = the weights that a 4-bit copy stands for."""
-    L, d, group = _q4_copy(codes, scales)
-    _shape("W", W, (L, d), *_BF16_BITS)
-    _here(W, codes, scales)
-    _check(load().elmo_q4_unpack(_ptr(codes), _ptr(scales), L, d, group, _ptr(W), _stream(stream)))
+    c, s, L, d, group = _q4_copy(codes, scales)
+    _check(load().elmo_q4_unpack(c, s, L, d, group, _arg("W", W, (L, d), _BF16_BITS), _stream(stream)))
 
 
 def elmo_q4_scores(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, Z: torch.Tensor, stream=None):
     """Z (fp32 [B, L], rows may have a pitch) = the scores of the queries X (bf16 [B, d]) against a 4-bit copy."""
-    L, d, group = _q4_copy(codes, scales)
+    c, s, L, d, group = _q4_copy(codes, scales)
     B = X.shape[0]
-    _shape("X", X, (B, d), *_BF16_BITS)
-    _shape("Z", Z, (B, L), torch.float32)
-    _here(codes, scales, X, Z)
-    z, ldz = _rows_ptr("Z", Z)
-    _check(load().elmo_q4_scores(_ptr(codes), _ptr(scales), L, d, group, _ptr(X), B, z, ldz, _stream(stream)))
-
-
-_SCORE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+    _check(load().elmo_q4_scores(c, s, L, d, group, _arg("X", X, (B, d), _BF16_BITS), B,
+                                 _arg("Z", Z, (B, L), _F32, pitch=True), _pitch(Z), _stream(stream)))
 
 
 def _given(rowptr, cols, B):
-    _shape("rowptr", rowptr, (B + 1,), torch.int32)
-    _shape("cols", cols, (cols.numel(),), torch.int32)
-    return cols.numel()
+    """(address of rowptr, of cols, nnz) of the given labels of B queries."""
+    nnz = cols.numel()
+    return _arg("rowptr", rowptr, (B + 1,), _I32), _arg("cols", cols, (nnz,), _I32) if nnz else None, nnz
 
 
 def _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp):
-    """Checks the outputs of a log-probability call; returns k."""
-    _shape("logp", logp, (nnz,), torch.float32)
-    _shape("lse", lse, (B,), torch.float32)
-    _shape("entropy", entropy, (B,), torch.float32)
+    """k and the addresses of the outputs of a log-probability call."""
     if (top_idx is None) != (top_logp is None):
         raise ValueError("top_idx and top_logp go together")
-    if top_idx is None:
-        return 0
-    k = top_idx.shape[-1]
-    _shape("top_idx", top_idx, (B, k), torch.int32)
-    _shape("top_logp", top_logp, (B, k), torch.float32)
-    return k
+    k = 0 if top_idx is None else top_idx.shape[-1]
+    p = _arg("logp", logp, (nnz,), _F32)
+    return (k, p if nnz else None, _arg("lse", lse, (B,), _F32), _arg("entropy", entropy, (B,), _F32),
+            _arg("top_idx", top_idx, (B, k), _I32) if k else None,
+            _arg("top_logp", top_logp, (B, k), _F32) if k else None)
 
 
 def elmo_score_logprobs_workspace_bytes(B: int, L: int, k: int) -> int:
@@ -441,18 +431,15 @@ def elmo_score_logprobs(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tenso
                         top_logp: torch.Tensor | None, workspace: torch.Tensor, stream=None):
     """Softmax statistics of rows of scores Z (fp32 or bf16 [B, L], rows may have a pitch): logp fp32 [nnz] of the
     given labels (CSR rowptr / cols, int32), lse and entropy fp32 [B], and the k best labels top_idx int32 [B, k]
-    with top_logp fp32 [B, k] (None: no list).  workspace: any tensor of at least
-    elmo_score_logprobs_workspace_bytes(B, L, k) bytes; see include/elmo.h."""
+    with top_logp fp32 [B, k] (None: no list).  workspace: uint8, at least
+    elmo_score_logprobs_workspace_bytes(B, L, k) of them; see include/elmo.h."""
     B, L = Z.shape
-    _shape("Z", Z, (B, L), *_SCORE_TYPES)
-    nnz = _given(rowptr, cols, B)
-    k = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
-    _here(Z, rowptr, cols, logp, lse, entropy, top_idx, top_logp, workspace)
-    z, ldz = _rows_ptr("Z", Z)
-    _check(load().elmo_score_logprobs(z, _SCORE_TYPES[Z.dtype], ldz, B, L, _ptr(rowptr), _ptr(cols) if nnz else None,
-                                      nnz, k, _ptr(logp) if nnz else None, _ptr(lse), _ptr(entropy),
-                                      _ptr(top_idx) if k else None, _ptr(top_logp) if k else None, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)))
+    z = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True)
+    rp, cs, nnz = _given(rowptr, cols, B)
+    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
+    n = workspace.numel()
+    _check(load().elmo_score_logprobs(z, _SCORE_TYPES[Z.dtype], _pitch(Z), B, L, rp, cs, nnz, k, p, l, h, ti, tl,
+                                      _arg("workspace", workspace, (n,), _U8), n, _stream(stream)))
 
 
 def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tensor, lse: torch.Tensor,
@@ -462,19 +449,15 @@ def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: to
     """dZ (Z's type and shape; may be Z) = the gradient of elmo_score_logprobs with regard to the scores, given the
     gradients g_logp fp32 [nnz], g_lse and g_entropy fp32 [B] of its outputs (None: zeros) and its lse and entropy."""
     B, L = Z.shape
-    _shape("Z", Z, (B, L), *_SCORE_TYPES)
-    _shape("dZ", dZ, (B, L), Z.dtype)
-    nnz = _given(rowptr, cols, B)
-    for name, t, n in (("lse", lse, B), ("entropy", entropy, B), ("g_logp", g_logp, nnz), ("g_lse", g_lse, B),
-                       ("g_entropy", g_entropy, B)):
-        if t is not None or name == "lse":
-            _shape(name, t, (n,), torch.float32)
-    _here(Z, rowptr, cols, lse, entropy, g_logp, g_lse, g_entropy, dZ)
-    z, ldz = _rows_ptr("Z", Z)
-    dz, lddz = _rows_ptr("dZ", dZ)
-    _check(load().elmo_score_logprobs_backward(z, _SCORE_TYPES[Z.dtype], ldz, B, L, _ptr(rowptr),
-                                               _ptr(cols) if nnz else None, nnz, _ptr(lse), _ptr(entropy),
-                                               _ptr(g_logp) if nnz else None, _ptr(g_lse), _ptr(g_entropy), dz, lddz,
+    z = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True)
+    rp, cs, nnz = _given(rowptr, cols, B)
+    maybe = lambda name, t, n: None if t is None else _arg(name, t, (n,), _F32)   # noqa: E731
+    g = maybe("g_logp", g_logp, nnz)
+    _check(load().elmo_score_logprobs_backward(z, _SCORE_TYPES[Z.dtype], _pitch(Z), B, L, rp, cs, nnz,
+                                               _arg("lse", lse, (B,), _F32), maybe("entropy", entropy, B),
+                                               g if nnz else None, maybe("g_lse", g_lse, B),
+                                               maybe("g_entropy", g_entropy, B),
+                                               _arg("dZ", dZ, (B, L), (Z.dtype,), pitch=True), _pitch(dZ),
                                                _stream(stream)))
 
 
@@ -485,13 +468,10 @@ def elmo_label_logprobs(head: Head, X: torch.Tensor, rowptr: torch.Tensor, cols:
     storing a score: logp fp32 [nnz] of the given labels (CSR rowptr / cols), lse and entropy fp32 [B], the k best
     labels top_idx int32 [B, k] with top_logp fp32 [B, k] (None: no list)."""
     B = X.shape[0]
-    _shape("X", X, (B, head.d), *_BF16_BITS)
-    nnz = _given(rowptr, cols, B)
-    k = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
-    _here(X, rowptr, cols, logp, lse, entropy, top_idx, top_logp)
-    _check(load().elmo_label_logprobs(head.handle, _ptr(X), B, _ptr(rowptr), _ptr(cols) if nnz else None, nnz, k,
-                                      _ptr(logp) if nnz else None, _ptr(lse), _ptr(entropy),
-                                      _ptr(top_idx) if k else None, _ptr(top_logp) if k else None, _stream(stream)))
+    rp, cs, nnz = _given(rowptr, cols, B)
+    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
+    _check(load().elmo_label_logprobs(head.handle, _arg("X", X, (B, head.d), _BF16_BITS), B, rp, cs, nnz, k, p, l, h, ti,
+                                      tl, _stream(stream)))
 
 
 def elmo_check_bounded_wait(limit_cycles: int, status: torch.Tensor, stream=None):

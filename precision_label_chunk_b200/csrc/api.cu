@@ -166,6 +166,14 @@ elmo_status check_q4(const void* codes, const void* scales, int64_t L, int32_t d
   return ELMO_OK;
 }
 
+// Lists of given labels of the log-probability calls.
+elmo_status check_given(const int32_t* cols, int32_t nnz) {
+  if (nnz < 0) return fail(ELMO_EINVAL, "nnz = %d < 0", nnz);
+  if (nnz > (1 << 30)) return fail(ELMO_EUNSUPPORTED, "nnz = %d above 2^30", nnz);
+  if (nnz > 0 && !cols) return fail(ELMO_EINVAL, "null cols with nnz > 0");
+  return ELMO_OK;
+}
+
 // Rows of scores and the lists of given labels (elmo_score_*).
 elmo_status check_scores(const void* Z, elmo_score_dtype zt, int64_t ldz, int32_t B, int64_t L, const int32_t* rowptr,
                          const int32_t* cols, int32_t nnz) {
@@ -175,9 +183,7 @@ elmo_status check_scores(const void* Z, elmo_score_dtype zt, int64_t ldz, int32_
   if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
   if (L < 1 || L >= ELMO_MAX_LABELS) return fail(ELMO_EINVAL, "L = %lld outside [1, 2^24)", (long long)L);
   if (ldz < L) return fail(ELMO_EINVAL, "pitch of Z = %lld below L = %lld", (long long)ldz, (long long)L);
-  if (nnz < 0) return fail(ELMO_EINVAL, "nnz = %d < 0", nnz);
-  if (nnz > 0 && !cols) return fail(ELMO_EINVAL, "null cols with nnz > 0");
-  return ELMO_OK;
+  return check_given(cols, nnz);
 }
 
 }  // namespace
@@ -706,14 +712,13 @@ elmo_status elmo_label_logprobs(elmo_head* h, const void* X_dev, int32_t B, cons
   if (!X_dev || !rowptr_dev) return fail(ELMO_EINVAL, "null X or rowptr");
   if (!aligned16(X_dev)) return fail(ELMO_EINVAL, "X is not 16-byte aligned");
   if (B < 1 || B > ELMO_MAX_PREDICT_BATCH) return fail(ELMO_EINVAL, "B = %d outside [1, %d]", B, ELMO_MAX_PREDICT_BATCH);
-  if (nnz < 0) return fail(ELMO_EINVAL, "nnz = %d < 0", nnz);
-  if (nnz > 0 && !cols_dev) return fail(ELMO_EINVAL, "null cols with nnz > 0");
+  elmo_status st = check_given(cols_dev, nnz);
+  if (st != ELMO_OK) return st;
   if (k < 0 || k > ELMO_MAX_TOPK || (int64_t)k > h->L) return fail(ELMO_EINVAL, "k = %d outside [0, min(L, %d)]", k, ELMO_MAX_TOPK);
   if (!lse_dev || !entropy_dev || (nnz > 0 && !logp_dev) || (k > 0 && (!top_idx_dev || !top_logp_dev)))
     return fail(ELMO_EINVAL, "null output");
   if (h->labels_total != h->L) return fail(ELMO_EUNSUPPORTED, "a head that is split over devices");
-  elmo_status st = check_device(h);
-  if (st != ELMO_OK) return st;
+  if ((st = check_device(h)) != ELMO_OK) return st;
   HeadImpl* hi = static_cast<HeadImpl*>(h);
   if ((st = ensure_lp(hi, elmo::label_logprobs_workspace(h, B, k))) != ELMO_OK) return st;
   ELMO_CUDA(elmo::launch_label_logprobs(h, static_cast<const uint16_t*>(X_dev), B, rowptr_dev, cols_dev, nnz, k,

@@ -43,6 +43,7 @@
 #include "elmo_common.cuh"
 #include "elmo_internal.h"
 #include "elmo_operators.h"
+#include "softmax.cuh"
 #include "tc_ptx.cuh"
 
 namespace elmo {
@@ -54,9 +55,7 @@ constexpr int kThreads = 384;             // warp 0 TMA, 1 MMA and TMEM, 2-9 epi
 constexpr int kMaxStages = 16;
 constexpr uint32_t kAccCol = 384;         // first accumulator column where X lies in TMEM
 constexpr long long kWait = 4000000000LL; // ~2 s
-constexpr float kFloor = -200.0f;         // z - m where e^(z - m) is 0 in fp32
 constexpr float kNoLabel = -3.0e38f;      // a score that e^ takes to 0 and whose product with it is 0
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr size_t kMaxima = size_t(256) << 20;   // bytes of block maxima, about
 constexpr int kJoinThreads = 512;
@@ -70,16 +69,6 @@ constexpr int kSegs = 74;                 // label segments of the exact path
 constexpr int kExactThreads = 256;
 constexpr int kExactChunk = 2048;
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // Doubles as whole numbers of the same order;
 // 0 for scores that are never listed (-inf, NaN); -0 and 0 are the same score
 __device__ __forceinline__ uint64_t ord64(double f) {
@@ -90,8 +79,6 @@ __device__ __forceinline__ uint64_t ord64(double f) {
 __device__ __forceinline__ double ord64_value(uint64_t k) {
   return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
 }
-
-struct Stat { float m, s, t; };
 
 struct Counts { uint32_t wmax; int32_t nfail, nitems; };
 
@@ -146,6 +133,7 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
   __shared__ float red[kPrepThreads / 32];
   __shared__ uint32_t mx;
   const int b = blockIdx.x, tid = threadIdx.x;
+  pdl_trigger();
   if (tid == 0) {
     if (b == 0) *A.counts = {0u, 0, 0};
     if (A.k > 0) A.done[b] = A.nnear[b] = 0;
@@ -216,82 +204,6 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   if (atomicCAS(status, 0, (int)ELMO_ETIMEOUT) == 0) status[1] = site;
 }
 
-// two fp32 operations an instruction
-struct f2 { uint64_t v; };
-__device__ __forceinline__ f2 pair(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(f2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-// A query's running softmax: scores are inv times the accumulators, m in the
-// accumulators' units, t = sum e^(z - m)(z - m) / inv.
-struct Soft {
-  float m = -INFINITY, s = 0.0f, t = 0.0f;
-  float c2, floor_v;                                   // inv log2(e); -200 / inv
-
-  // 32 accumulators; returns their maximum
-  __device__ __forceinline__ float add32(const uint32_t (&v)[32]) {
-    float x[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      x[c] = fmaxf(fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 8])),
-                   fmaxf(__uint_as_float(v[c + 16]), __uint_as_float(v[c + 24])));
-    const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (mx > m) {
-      if (m > -INFINITY) {
-        const float dm = fmaxf(m - mx, floor_v), c = ex2(dm * c2);
-        t = c * fmaf(s, dm, t);
-        s *= c;
-      }
-      m = mx;
-    }
-    const float m0 = m > -INFINITY ? m : 0.0f;
-    const f2 nm = pair(-m0, -m0), cc = pair(c2, c2);
-    f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const f2 d = add2(pair(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), nm);
-      float a, b;
-      unpair(mul2(d, cc), a, b);
-      const f2 e = pair(ex2(a), ex2(b));
-      ps[c & 1] = add2(ps[c & 1], e);
-      pt[c & 1] = fma2(e, d, pt[c & 1]);
-    }
-    float s0, s1, t0, t1;
-    unpair(add2(ps[0], ps[1]), s0, s1);
-    unpair(add2(pt[0], pt[1]), t0, t1);
-    float tt = t0 + t1;
-    if (tt != tt) {                                    // a score of -inf (0 times infinity), or a NaN
-      tt = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float d = max_nan(__uint_as_float(v[c]) - m0, floor_v);
-        tt = fmaf(ex2(d * c2), d, tt);
-      }
-    }
-    s += s0 + s1;
-    t += tt;
-    return mx;
-  }
-};
-
 // kFp8: 8-bit head (kW5: E5M2 weights).  kXs = 0: d <= 768, X (two 8-bit or
 // one bf16 operand, 2 d bytes a query) stays in TMEM columns 0..383 and tiles
 // are 64 labels with two accumulators in the rest; kXs = 1: wider heads, X
@@ -336,6 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S->tmem_base;
+  pdl_trigger();
+  // W is no other kernel's here: its copies start while the operands are still
+  // being formed, everything else waits for them
+  if (warp != 0 || kXs) pdl_wait();
 
   if (!kXs) {
     if (warp >= 2 && warp < 6) {                       // query r of the panel into lane r
@@ -358,7 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
     }
     tc_fence_before();
-    __syncthreads();
+    // the TMA warp does not come here: the others' barrier
+    if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
     tc_fence_after();
   }
 
@@ -450,9 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, r = quad * 32 + lane, row = p * 128 + r;
     const bool live = row < A.B;
     const float inv = live ? A.xinv[row] : 1.0f;
-    Soft soft;
-    soft.c2 = inv * kLog2e;
-    soft.floor_v = kFloor / inv;
+    Soft soft(inv);
     float* bm = A.bmax + ((size_t)row * 2 + par) * A.nblkp;
     float win[8];                                      // maxima of the aligned eight blocks under way
     uint32_t nt = 0;
@@ -468,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int u = 0; u < kN / 64; ++u) {
           __syncwarp();
-          uint32_t v[2][32];
+          uint32_t raw[2][32];
           const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (kXs ? 0 : kAccCol) + par * kN + u * 64;
-          tmem_ld32(at, v[0]);
-          tmem_ld32(at + 32, v[1]);
+          tmem_ld32(at, raw[0]);
+          tmem_ld32(at + 32, raw[1]);
           tmem_wait_ld();
           if (u == kN / 64 - 1) {
             tc_fence_before();
@@ -483,11 +398,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (l0 + 64 > A.L) {                         // past the end there are no labels
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (l0 + c >= A.L) v[c >> 5][c & 31] = __float_as_uint(kNoLabel);
-            if (l0 >= A.L) continue;
+              if (l0 + c >= A.L) raw[c >> 5][c & 31] = __float_as_uint(kNoLabel);
           }
-          best = fmaxf(best, soft.add32(v[0]));
-          if (l0 + 32 < A.L) best = fmaxf(best, soft.add32(v[1]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (l0 + 32 * h >= A.L) break;
+            float v[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[h][c]);
+            const float mx = max32(v);
+            best = fmaxf(best, mx);
+            soft.add32<false>(v, mx);
+          }
         }
       }
       if (A.k > 0 && live) {
@@ -645,7 +567,7 @@ __device__ __forceinline__ float max_weight(uint32_t code, int fmt) {
 
 // ---------------------------------------------------------------- 3. join
 struct SmemB {
-  float gbest[kGroups];
+  alignas(16) float gbest[kGroups];
   float low;
 };
 
@@ -664,7 +586,11 @@ __device__ __forceinline__ float lower_bound_kth(SmemB* S, float best, int k) {
   if (tid < kGroups) {
     const float mine = S->gbest[tid];
     int above = 0, same = 0;
-    for (int j = 0; j < kGroups; ++j) { above += S->gbest[j] > mine; same += S->gbest[j] == mine; }
+    for (int j = 0; j < kGroups; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(S->gbest + j);
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      same += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+    }
     if (above < k && above + same >= k) S->low = mine;
   }
   __syncthreads();
@@ -687,7 +613,8 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   __shared__ SmemB S;
   __shared__ int32_t blocks[kMaxBlocks];
   constexpr int kW = kJoinThreads / 32;
-  __shared__ double stat[2], ws[kW], wt[kW];
+  constexpr int kEarly = 512;
+  __shared__ double stat[2], ws[kW], wt[kW], early[kEarly];
   __shared__ float wm[kW];
   __shared__ int nblocks, at0;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -697,7 +624,20 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
   }
   if (tid == 0) nblocks = 0;
+  __syncthreads();
+  // the given labels' scores need only X and W: the first kEarly of them while
+  // the score pass still runs elsewhere
+  const int e0 = min(max(A.rowptr[b], 0), A.nnz), e1 = min(A.rowptr[b + 1], A.nnz), ee = min(e1, e0 + kEarly);
+  auto given = [&](int e) {
+    const int64_t l = (int64_t)A.cols[e] - A.label_base;
+    return l >= 0 && l < A.L ? exact_score<kFormat>(xs, A.W, l, A.d, lane) : 0.0;
+  };
+  for (int e = e0 + warp; e < ee; e += kW) {
+    const double z = given(e);
+    if (lane == 0) early[e - e0] = z;
+  }
   pdl_wait();
+  pdl_trigger();
   const bool bad = A.rflag[b] != 0;
   {
     // at most two partial sums of a thread: 2 G <= 2 SMs
@@ -814,19 +754,21 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     }
   }
 
-  const int e0 = max(A.rowptr[b], 0), e1 = min(A.rowptr[b + 1], A.nnz);
-  for (int e = e0 + warp; e < e1; e += kW) {
+  auto put = [&](int e, double z) {
     const int64_t id = A.cols[e], l = id - A.label_base;
-    float r = NAN;
+    float r = (float)(z - m - logs);
     if (id < 0 || id >= A.labels_total) {
-      if (lane == 0 && atomicCAS(A.status, 0, (int)ELMO_EDATA) == 0) A.status[1] = e;
-    } else if (l < 0 || l >= A.L) {
-      r = -INFINITY;                                   // another device's label
-    } else {
-      const double z = exact_score<kFormat>(xs, A.W, l, A.d, lane);
-      r = z == -INFINITY && !isnan(m + logs) ? -INFINITY : (float)(z - m - logs);
+      r = NAN;
+      if (atomicCAS(A.status, 0, (int)ELMO_EDATA) == 0) A.status[1] = e;
+    } else if (l < 0 || l >= A.L || (z == -INFINITY && !isnan(m + logs))) {
+      r = -INFINITY;                                   // another device's label, or a masked one
     }
-    if (lane == 0) A.logp[e] = r;
+    A.logp[e] = r;
+  };
+  for (int e = e0 + tid; e < ee; e += kJoinThreads) put(e, early[e - e0]);
+  for (int e = e0 + kEarly + warp; e < e1; e += kW) {
+    const double z = given(e);
+    if (lane == 0) put(e, z);
   }
 }
 
@@ -838,6 +780,7 @@ template <int kFormat>
 __global__ void __launch_bounds__(kNearThreads) label_near_kernel(const Args A, int tile) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
+  pdl_trigger();
   const int per = A.pairs * tile / kNearAt;
   const int64_t work = (int64_t)A.counts->nitems * per;
   for (int64_t w = (int64_t)blockIdx.x * (kNearThreads / 32) + (threadIdx.x >> 5); w < work;
@@ -884,6 +827,7 @@ __global__ void __launch_bounds__(kNearThreads) label_rank_kernel(const Args A) 
   }
   if (tid == 0) nexact = 0;
   pdl_wait();
+  pdl_trigger();
   if (A.listed[b] == 0) return;                          // answered, or a failed query already
   const int near = A.nnear[b];
   bool ok = near >= A.k && near <= kMaxNear;
@@ -1120,25 +1064,22 @@ cudaError_t run_pass(elmo_head* h, Args A, cudaStream_t s) {
     if (kFp8 && (e = map(&tmB, A.xb, A.B, 128)) != cudaSuccess) return e;
   }
   auto kern = label_score_kernel<kFp8, kW5, kXs>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> seen{0};
+  if ((e = allow_smem(kern, (int)kSmemMost, seen)) != cudaSuccess) return e;
   const int P = (A.B + 127) / 128;
-  kern<<<P * A.G, kThreads, fixed + A.stages * stage, s>>>(tmW, tmA, tmB, A);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(P * A.G), kThreads, fixed + A.stages * stage, s, tmW, tmA, tmB, A);
 }
 
 template <int kFormat>
 cudaError_t run_join(elmo_head* h, const Args& A, cudaStream_t s) {
   const size_t xbytes = sizeof(float) * (size_t)h->d;
-  label_join_kernel<kFormat><<<A.B, kJoinThreads, xbytes, s>>>(A);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(label_join_kernel<kFormat>, dim3(A.B), kJoinThreads, xbytes, s, A);
   if (e != cudaSuccess || A.k == 0) return e;
-  label_near_kernel<kFormat><<<h->num_sms * 4, kNearThreads, 0, s>>>(A, tile_labels(h));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  label_rank_kernel<kFormat><<<A.B, kNearThreads, xbytes, s>>>(A);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  label_exact_kernel<kFormat><<<h->num_sms * 2, kExactThreads, xbytes, s>>>(A);
-  return cudaGetLastError();
+  e = launch_after(label_near_kernel<kFormat>, dim3(h->num_sms * 4), kNearThreads, 0, s, A, tile_labels(h));
+  if (e != cudaSuccess) return e;
+  e = launch_after(label_rank_kernel<kFormat>, dim3(A.B), kNearThreads, xbytes, s, A);
+  if (e != cudaSuccess) return e;
+  return launch_after(label_exact_kernel<kFormat>, dim3(h->num_sms * 2), kExactThreads, xbytes, s, A);
 }
 
 }  // namespace

@@ -21,29 +21,18 @@
 #include "elmo_common.cuh"
 #include "elmo_internal.h"
 #include "elmo_operators.h"
+#include "softmax.cuh"
 #include "tc_ptx.cuh"
 
 namespace elmo {
 namespace {
 
+using namespace tc;
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 1024;              // scores of a block
-constexpr float kFloor = -200.0f;         // z - m is cut here: e^-200 is 0 in fp32, and -inf 0 never forms
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSplit = 512;
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// max(a, b), NaN if either is
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // A score's place in the order as a whole number: larger is better, 0 for a
 // score that is never listed (-inf, NaN).  -0 and 0 are the same score.
@@ -57,9 +46,6 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
   return order ? ((uint64_t)order << 32) | (0xFFFFFFFFu - index) : 0ull;
 }
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
-
-// Row statistics with the maximum: sums of e^(z - m) and e^(z - m)(z - m).
-struct Stat { float m, s, t; };
 
 template <typename T> __device__ __forceinline__ float score_at(const T* z, int64_t i);
 template <> __device__ __forceinline__ float score_at<float>(const float* z, int64_t i) { return z[i]; }
@@ -125,58 +111,37 @@ struct Args {
   Stat* part;             // [B][splits]
 };
 
-// The pass over the row: the CTA's warps take its blocks in turn.  HBM-bound:
-// every score is read once, in 16-byte loads, 128 (fp32) or 64 (bf16) bytes
-// of a thread in flight.
+// The pass over a part of a row: the CTA's warps take its blocks in turn.
+// HBM-bound: every score is read once, in 16-byte loads, 128 (fp32) or 64
+// (bf16) bytes of a thread in flight; bf16 scores leave 1.4 exponentials of
+// the special-function unit's 1.9 a clock and SM.
 template <typename T>
-__device__ __forceinline__ Stat scan_row(const Args& A, const T* z, int shift, int64_t b, int split, Stat* red) {
+__device__ __forceinline__ Stat scan_row(const Args& A, const T* z, int shift, int64_t b, int64_t blk0, int64_t blk1,
+                                         Stat* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY, s = 0.0f, t = 0.0f;
-  for (int64_t blk = (int64_t)split * kWarps + warp; blk < A.nblk; blk += (int64_t)A.splits * kWarps) {
+  Soft soft(1.0f);
+  for (int64_t blk = blk0 + warp; blk < blk1; blk += kWarps) {
     float v[32];
     load_block(z, A.L, shift, blk, lane, v);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaxf(fmaxf(v[e], v[e + 8]), fmaxf(v[e + 16], v[e + 24]));
-    float bm = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
-    if (lane == 0) A.bmax[b * A.nblk + blk] = bm;
-    if (bm > m) {
-      if (m > -INFINITY) {
-        const float d = fmaxf(m - bm, kFloor), c = ex2(d * kLog2e);
-        t = c * fmaf(s, d, t);
-        s *= c;
-      }
-      m = bm;
+    const float mx = max32(v);
+    soft.add32<true>(v, mx);
+    if (A.k > 0) {
+      float bm = mx;
+      for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
+      if (lane == 0) A.bmax[b * A.nblk + blk] = bm;
     }
-    const float m0 = m > -INFINITY ? m : 0.0f;
-    float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f}, pt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float d = max_nan(v[e] - m0, kFloor);
-      const float p = ex2(d * kLog2e);
-      ps[e & 3] += p;
-      pt[e & 3] = fmaf(p, d, pt[e & 3]);
-    }
-    s += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-    t += (pt[0] + pt[1]) + (pt[2] + pt[3]);
   }
-  for (int o = 16; o > 0; o >>= 1) {      // a warp's lanes share m
-    s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xFFFFFFFFu, soft.m, o), os = __shfl_xor_sync(0xFFFFFFFFu, soft.s, o),
+                ot = __shfl_xor_sync(0xFFFFFFFFu, soft.t, o);
+    soft.join(om, os, ot);
   }
-  if (lane == 0) red[warp] = {m, s, t};
   __syncthreads();
-  Stat r{-INFINITY, 0.0f, 0.0f};
-  for (int w = 0; w < kWarps; ++w) r.m = fmaxf(r.m, red[w].m);
-  for (int w = 0; w < kWarps; ++w) {
-    const Stat p = red[w];
-    if (p.m == -INFINITY) { r.s += p.s; continue; }       // 0, or NaN where the warp saw nothing but NaN
-    const float d = fmaxf(p.m - r.m, kFloor), c = ex2(d * kLog2e);
-    r.s = fmaf(p.s, c, r.s);
-    r.t = fmaf(c, fmaf(p.s, d, p.t), r.t);
-  }
-  return r;
+  if (lane == 0) red[warp] = {soft.m, soft.s, soft.t};
+  __syncthreads();
+  Soft all(1.0f);
+  for (int w = 0; w < kWarps; ++w) all.join(red[w].m, red[w].s, red[w].t);
+  return {all.m, all.s, all.t};
 }
 
 // ---------------------------------------------------------------- the row's answers
@@ -235,16 +200,37 @@ __device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift
   }
   if (tid == 0) { S->tau = 0; S->n = 0; }
   __syncthreads();
-  if (tid < kGroups) {
-    const uint64_t mine = S->gbest[tid];
-    int rank = 0;
-    for (int j = 0; j < kGroups; ++j) rank += S->gbest[j] > mine;
-    if (mine && rank == k - 1) S->tau = mine;
-  }
-  __syncthreads();
-  const uint64_t tau = S->tau;                       // 0: fewer than k groups hold a score
+  auto kth_group = [&] {                             // tau <- the k-th best of the groups
+    if (tid < kGroups) {
+      const uint64_t mine = S->gbest[tid];
+      int rank = 0;
+      for (int j = 0; j < kGroups; ++j) rank += S->gbest[j] > mine;
+      if (mine && rank == k - 1) S->tau = mine;
+    }
+    __syncthreads();
+  };
+  kth_group();
+  const uint64_t tau = S->tau;                       // 0: fewer than k blocks hold a score
   // k scores are at least the score of tau's block
   uint64_t floor_key = tau & 0xFFFFFFFF00000000ull;
+  if (tau == 0) {                                    // few blocks: groups of pairs of threads, a thread's best score
+    uint64_t best = 0;
+    for (int64_t blk = warp; blk < A.nblk; blk += kWarps) {
+      float v[32];
+      load_block(z, A.L, shift, blk, lane, v);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
+        best = c > best ? c : best;
+      }
+    }
+    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
+    best = other > best ? other : best;
+    if (tid % 2 == 0) S->gbest[tid / 2] = best;
+    __syncthreads();
+    kth_group();
+    floor_key = S->tau;
+  }
   // the blocks from tau's up, a warp each
   for (int j0 = 0; j0 < A.nblk; j0 += kWarps * 32) {
     const int j = j0 + warp * 32 + lane;
@@ -348,8 +334,10 @@ __global__ void __launch_bounds__(kThreads) score_scan_kernel(const Args A) {
   __shared__ Stat red[kWarps];
   const int64_t b = blockIdx.y;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
-  const Stat r = scan_row(A, z, shift_of(z), b, blockIdx.x, red);
-  if (threadIdx.x == 0) A.part[b * A.splits + blockIdx.x] = r;
+  pdl_trigger();
+  const int64_t n = A.nblk, i = blockIdx.x;
+  const Stat r = scan_row(A, z, shift_of(z), b, n * i / A.splits, n * (i + 1) / A.splits, red);
+  if (threadIdx.x == 0) A.part[b * A.splits + i] = r;
 }
 
 template <typename T>
@@ -359,6 +347,7 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(const Args A) {
   const int64_t b = blockIdx.x;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
   const Stat* part = A.part + b * A.splits;
+  pdl_wait();
   float mf = -INFINITY;
   for (int i = tid; i < A.splits; i += kThreads) mf = fmaxf(mf, part[i].m);
   for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xFFFFFFFFu, mf, o));
@@ -392,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) score_row_kernel(const Args A) {
   const int64_t b = blockIdx.x;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
   const int shift = shift_of(z);
-  const Stat r = scan_row(A, z, shift, b, 0, S.row);
+  const Stat r = scan_row(A, z, shift, b, 0, A.nblk, S.row);
   __syncthreads();
   finish_row(A, z, shift, b, r.m, r.s, r.t, &S);
 }
@@ -435,6 +424,15 @@ __global__ void __launch_bounds__(kThreads) score_backward_kernel(const BwdArgs 
   const int64_t first = (int64_t)blockIdx.x * kSeg - shift;       // the segment's labels: [first, first + kSeg)
   const float lse = A.lse[b];
   const bool dead = isinf(lse);                                   // no label, or no softmax: no gradient
+
+  // the scores before anything that waits for the row's lists
+  constexpr int kVecs = kSeg / (kThreads * kE);
+  const bool whole = first >= 0 && first + kSeg <= A.L && shift_of(dz) == shift;
+  uint4 q[kVecs];
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(z + first) + i * kThreads + tid);
+  }
 
   double sum = 0.0;
   bool any = false;
@@ -482,39 +480,44 @@ __global__ void __launch_bounds__(kThreads) score_backward_kernel(const BwdArgs 
   const float gH = A.g_entropy ? A.g_entropy[b] : 0.0f;
   const float H = A.g_entropy ? A.entropy[b] : 0.0f;
   const float c0 = (float)((A.g_lse ? (double)A.g_lse[b] : 0.0) - sum - (double)gH * (double)H);
-  auto grad = [&](float x, int i) {
-    const float d = max_nan(x - lse, kFloor);
-    const float r = ex2(d * kLog2e) * fmaf(-gH, d, c0);
-    return dead ? 0.0f : any ? r + addend[i] : r;
+  auto grad = [&](float x) {
+    const float d = max_nan(x - lse, kSoftFloor);
+    return ex2(d * kLog2e) * fmaf(-gH, d, c0);
   };
-  if (shift_of(dz) == shift) {
-#pragma unroll 2
-    for (int i0 = tid * kE; i0 < kSeg; i0 += kThreads * kE) {
-      const int64_t l = first + i0;
-      if (l >= 0 && l + kE <= A.L) {
-        const uint4 q = *reinterpret_cast<const uint4*>(z + l);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        uint32_t o[4];
+  auto grad2 = [&](float x0, float x1, float& r0, float& r1) {
+    float d0, d1, a0, a1;
+    unpair(add2(pair(x0, x1), pair(-lse, -lse)), d0, d1);
+    const f2 d = pair(max_nan(d0, kSoftFloor), max_nan(d1, kSoftFloor));
+    unpair(mul2(d, pair(kLog2e, kLog2e)), a0, a1);
+    unpair(mul2(pair(ex2(a0), ex2(a1)), fma2(pair(-gH, -gH), d, pair(c0, c0))), r0, r1);
+  };
+  if (whole && !dead) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (sizeof(T) == 4) {
-            o[e] = __float_as_uint(grad(__uint_as_float(w[e]), i0 + e));
-          } else {
-            const float lo = grad(__uint_as_float(w[e] << 16), i0 + 2 * e);
-            const float hi = grad(__uint_as_float(w[e] & 0xFFFF0000u), i0 + 2 * e + 1);
-            o[e] = pack_bf16x2(hi, lo);
-          }
-        }
-        *reinterpret_cast<uint4*>(dz + l) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        for (int e = 0; e < kE; ++e)
-          if (l + e >= 0 && l + e < A.L) put_grad(dz + l + e, grad(score_at(z, l + e), i0 + e));
+    for (int i = 0; i < kVecs; ++i) {
+      const int i0 = (i * kThreads + tid) * kE;
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      float r[kE];
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        if (sizeof(T) == 4) grad2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]), r[2 * e], r[2 * e + 1]);
+        else grad2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u), r[2 * e], r[2 * e + 1]);
       }
+      if (any) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) r[e] += addend[i0 + e];
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = sizeof(T) == 4 ? __float_as_uint(r[e]) : pack_bf16x2(r[(2 * e + 1) % kE], r[(2 * e) % kE]);
+      __stcs(reinterpret_cast<uint4*>(dz + first) + i * kThreads + tid, make_uint4(o[0], o[1], o[2], o[3]));
     }
   } else {
     for (int i = tid; i < kSeg; i += kThreads) {
       const int64_t l = first + i;
-      if (l >= 0 && l < A.L) put_grad(dz + l, grad(score_at(z, l), i));
+      if (l < 0 || l >= A.L) continue;
+      float r = dead ? 0.0f : grad(score_at(z, l));
+      if (any) r += addend[i];
+      put_grad(dz + l, r);
     }
   }
 }
@@ -524,15 +527,8 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // blocks of a row, wherever its first score lies
 int32_t blocks_of(int64_t L) { return (int32_t)((L + 7 + kBlock - 1) / kBlock); }
 
-int sms_of_device() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
-  return n;
-}
-
 template <typename T>
-cudaError_t run_scores(Args A, int sms, cudaStream_t s) {
+cudaError_t run_scores(const Args& A, cudaStream_t s) {
   if (A.splits == 1) {
     score_row_kernel<T><<<A.B, kThreads, 0, s>>>(A);
     return cudaGetLastError();
@@ -540,8 +536,7 @@ cudaError_t run_scores(Args A, int sms, cudaStream_t s) {
   score_scan_kernel<T><<<dim3(A.splits, A.B), kThreads, 0, s>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  score_join_kernel<T><<<A.B, kThreads, 0, s>>>(A);
-  return cudaGetLastError();
+  return launch_after(score_join_kernel<T>, dim3(A.B), kThreads, 0, s, A);
 }
 
 }  // namespace
@@ -562,15 +557,16 @@ cudaError_t launch_score_logprobs(const void* Z, bool bf16, int64_t ldz, int32_t
   A.nblk = blocks_of(L);
   A.bmax = static_cast<float*>(work);
   A.part = reinterpret_cast<Stat*>(static_cast<char*>(work) + align256(sizeof(float) * (size_t)B * A.nblk));
-  const int sms = sms_of_device();
-  // enough CTAs to fill the machine four deep, at least a block for every warp
-  int64_t splits = ((int64_t)sms * 4 + B - 1) / B;
-  const int64_t most = (A.nblk + kWarps - 1) / kWarps;
-  if (splits > most) splits = most;
+  const int sms = current_sms();
+  // about 32 CTAs an SM, so that the last ones to end leave little idle, of at
+  // least a block a warp
+  int64_t per = ((int64_t)A.nblk * B + (int64_t)sms * 32 - 1) / ((int64_t)sms * 32);
+  if (per < kWarps) per = kWarps;
+  int64_t splits = (A.nblk + per - 1) / per;
   if (splits > kMaxSplit) splits = kMaxSplit;
   if (A.nblk <= 4 * kWarps) splits = 1;
   A.splits = (int32_t)splits;
-  return bf16 ? run_scores<uint16_t>(A, sms, s) : run_scores<float>(A, sms, s);
+  return bf16 ? run_scores<uint16_t>(A, s) : run_scores<float>(A, s);
 }
 
 cudaError_t launch_score_backward(const void* Z, bool bf16, int64_t ldz, int32_t B, int64_t L, const int32_t* rowptr,

@@ -144,15 +144,8 @@ __global__ void __launch_bounds__(kPackThreads) q4_unpack_kernel(const uint2* __
   }
 }
 
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
-  return n;
-}
-
 int flat_grid(int64_t threads) {
-  const int64_t want = (threads + kPackThreads - 1) / kPackThreads, most = (int64_t)device_sms() * 16;
+  const int64_t want = (threads + kPackThreads - 1) / kPackThreads, most = (int64_t)current_sms() * 16;
   return (int)(want < most ? want : most);
 }
 
@@ -485,7 +478,8 @@ cudaError_t run_q4(const uint8_t* codes, Q4Args A, int sms, cudaStream_t s) {
   cudaError_t e = make_tma_map_2d(&tm, codes, 1, (uint64_t)A.d / 2, (uint64_t)A.L, (uint64_t)A.d / 2, kTile);
   if (e != cudaSuccess) return e;
   auto k = q4_scores_kernel<kG, kMT, kNB, kWarps>;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQSmem)) != cudaSuccess) return e;
+  static std::atomic<uint64_t> seen{0};
+  if ((e = allow_smem(k, (int)kQSmem, seen)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(T < sms ? T : sms), (unsigned)((A.B + 8 * kNB - 1) / (8 * kNB)));
   k<<<grid, 32 * (kWarps + 1), smem, s>>>(tm, A);
   return cudaGetLastError();
@@ -493,7 +487,7 @@ cudaError_t run_q4(const uint8_t* codes, Q4Args A, int sms, cudaStream_t s) {
 
 template <int kG>
 cudaError_t run_q4_group(const uint8_t* codes, const Q4Args& A, cudaStream_t s) {
-  const int sms = device_sms();
+  const int sms = current_sms();
   // queries of one pass over the codes: as many as the fragments of X leave room for
   const int nb = (A.B + 7) / 8;
   const size_t x1 = (size_t)A.d * 16;                // X fragments of 8 queries

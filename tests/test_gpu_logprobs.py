@@ -344,7 +344,7 @@ def test_refusals():
     elmo.elmo_score_logprobs(**good)
     for bad in [dict(Z=f(3, 100, dt=torch.float16)), dict(Z=f(100, 3).T), dict(rowptr=i(3)), dict(cols=f(5)),
                 dict(logp=f(4)), dict(lse=f(4)), dict(top_idx=i(3, 3)), dict(top_idx=None), dict(entropy=f(3).cpu()),
-                dict(Z=f(1, 100).expand(3, 100))]:
+                dict(Z=f(1, 100).expand(3, 100)), dict(workspace=work.float())]:
         with pytest.raises((ValueError, TypeError)):
             elmo.elmo_score_logprobs(**{**good, **bad})
     with pytest.raises(elmo.ElmoError, match="workspace"):
