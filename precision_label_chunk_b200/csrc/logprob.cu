@@ -111,49 +111,113 @@ struct Args {
   Stat* part;             // [B][splits]
 };
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Adds a thread's 32 scores of a block to its sums; returns their maximum.
+//
+// bf16: two scores an instruction as far as that goes, or the issue slots bind
+// (256 rows of 500K: 70 us with seven and more a score, 56 with five and a half):
+// the maximum of the pairs, and -inf raised to the lowest finite number, whose
+// e^ is 0 and whose product with 0 is 0.  Where that number itself may be the
+// row's maximum, and on infinities and NaN, the sums are formed one by one.
+__device__ __forceinline__ float add_block(Soft& soft, const float* z, int64_t L, int shift, int64_t blk, int lane) {
+  float v[32];
+  load_block(z, L, shift, blk, lane, v);
+  const float mx = max32(v);
+  soft.add32<true>(v, mx);
+  return mx;
+}
+__device__ __forceinline__ float add_block(Soft& soft, const uint16_t* z, int64_t L, int shift, int64_t blk, int lane) {
+  const int64_t first = blk * kBlock - shift;
+  float v[32];
+  if (first < 0 || first + kBlock > L) {
+    load_block(z, L, shift, blk, lane, v);
+    const float mx = max32(v);
+    soft.add32<true>(v, mx);
+    return mx;
+  }
+  const uint4* p = reinterpret_cast<const uint4*>(z + first) + lane;
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 q = __ldg(p + 32 * i);
+    w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+  }
+  uint32_t x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = max_bf16x2(max_bf16x2(w[i], w[i + 4]), max_bf16x2(w[i + 8], w[i + 12]));
+  x[0] = max_bf16x2(max_bf16x2(x[0], x[1]), max_bf16x2(x[2], x[3]));
+  // all NaN: the maximum is NaN, which raises nothing
+  const float mx = fmaxf(fmaxf(__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xFFFF0000u)), -INFINITY);
+  if (mx > soft.m) soft.raise(mx);
+  const float m0 = soft.m > -INFINITY ? soft.m : 0.0f;
+  float ss, tt;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u = max_nan_bf16x2(w[i], 0xFF7FFF7Fu);
+    v[2 * i] = __uint_as_float(u << 16);
+    v[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
+  }
+  soft.sums32<false>(v, m0, ss, tt);
+  if (tt != tt || m0 < -1.0e38f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    soft.slow32(v, m0, ss, tt);
+  }
+  soft.s += ss;
+  soft.t += tt;
+  return mx;
+}
+
 // The pass over a part of a row: the CTA's warps take its blocks in turn.
 // HBM-bound: every score is read once, in 16-byte loads, 128 (fp32) or 64
-// (bf16) bytes of a thread in flight; bf16 scores leave 1.4 exponentials of
-// the special-function unit's 1.9 a clock and SM.
+// (bf16) bytes of a thread in flight.
 template <typename T>
 __device__ __forceinline__ Stat scan_row(const Args& A, const T* z, int shift, int64_t b, int64_t blk0, int64_t blk1,
                                          Stat* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Soft soft(1.0f);
   for (int64_t blk = blk0 + warp; blk < blk1; blk += kWarps) {
-    float v[32];
-    load_block(z, A.L, shift, blk, lane, v);
-    const float mx = max32(v);
-    soft.add32<true>(v, mx);
+    float bm = add_block(soft, z, A.L, shift, blk, lane);
     if (A.k > 0) {
-      float bm = mx;
       for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
       if (lane == 0) A.bmax[b * A.nblk + blk] = bm;
     }
   }
-  for (int o = 16; o > 0; o >>= 1) {
-    const float om = __shfl_xor_sync(0xFFFFFFFFu, soft.m, o), os = __shfl_xor_sync(0xFFFFFFFFu, soft.s, o),
-                ot = __shfl_xor_sync(0xFFFFFFFFu, soft.t, o);
-    soft.join(om, os, ot);
-  }
-  __syncthreads();
+  soft.join_warp();
   if (lane == 0) red[warp] = {soft.m, soft.s, soft.t};
   __syncthreads();
+  const Stat q = red[lane % kWarps];
   Soft all(1.0f);
-  for (int w = 0; w < kWarps; ++w) all.join(red[w].m, red[w].s, red[w].t);
+  if (lane < kWarps) { all.m = q.m; all.s = q.s; all.t = q.t; }
+  all.join_warp();
   return {all.m, all.s, all.t};
 }
 
 // ---------------------------------------------------------------- the row's answers
 constexpr int kGroups = 128;              // a lower bound on the k-th best block comes from the groups' best
 constexpr int kCand = 4096;               // keys the selection holds
+constexpr int kList = 512;                // blocks that may hold them
 constexpr int kBatch = kThreads * 8;      // keys added between two looks at the room
 
 struct SmemJ {
   uint64_t cand[kCand];
   uint64_t gbest[kGroups];
   uint64_t tau;
-  int n;
+  int32_t blocks[kList];
+  int n, nb;
   double red[3 * kWarps];
   Stat row[kWarps];
 };
@@ -176,62 +240,17 @@ __device__ __forceinline__ void sort_desc(uint64_t* cand, int n) {
   }
 }
 
-// Labels and log probabilities of the row's k best scores.  Every thread of
-// the CTA calls it.
+// The scores from floor_key up of the blocks from tau up, where they are more
+// than fit: in batches, of which the k best stay.
 template <typename T>
-__device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift, int64_t b, double m, double logs,
-                                            SmemJ* S) {
+__device__ __noinline__ void best_of_many(const Args& A, const T* z, int shift, int64_t b, uint64_t tau,
+                                          uint64_t floor_key, SmemJ* S) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int k = A.k;
   const float* bm = A.bmax + b * A.nblk;
-  // tau: the k-th best of the groups' best blocks is at most the k-th best block
-  if (A.nblk <= kGroups) {
-    if (tid < kGroups) S->gbest[tid] = tid < A.nblk ? key_of(order_of(__ldcg(bm + tid)), (uint32_t)tid) : 0ull;
-  } else {
-    const int grp = tid / (kThreads / kGroups);
-    uint64_t best = 0;
-    for (int j = grp + kGroups * (tid % (kThreads / kGroups)); j < A.nblk; j += kThreads) {
-      const uint64_t c = key_of(order_of(__ldcg(bm + j)), (uint32_t)j);
-      best = c > best ? c : best;
-    }
-    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
-    best = other > best ? other : best;
-    if (tid % 2 == 0) S->gbest[grp] = best;
-  }
-  if (tid == 0) { S->tau = 0; S->n = 0; }
   __syncthreads();
-  auto kth_group = [&] {                             // tau <- the k-th best of the groups
-    if (tid < kGroups) {
-      const uint64_t mine = S->gbest[tid];
-      int rank = 0;
-      for (int j = 0; j < kGroups; ++j) rank += S->gbest[j] > mine;
-      if (mine && rank == k - 1) S->tau = mine;
-    }
-    __syncthreads();
-  };
-  kth_group();
-  const uint64_t tau = S->tau;                       // 0: fewer than k blocks hold a score
-  // k scores are at least the score of tau's block
-  uint64_t floor_key = tau & 0xFFFFFFFF00000000ull;
-  if (tau == 0) {                                    // few blocks: groups of pairs of threads, a thread's best score
-    uint64_t best = 0;
-    for (int64_t blk = warp; blk < A.nblk; blk += kWarps) {
-      float v[32];
-      load_block(z, A.L, shift, blk, lane, v);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
-        best = c > best ? c : best;
-      }
-    }
-    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
-    best = other > best ? other : best;
-    if (tid % 2 == 0) S->gbest[tid / 2] = best;
-    __syncthreads();
-    kth_group();
-    floor_key = S->tau;
-  }
-  // the blocks from tau's up, a warp each
+  if (tid == 0) S->n = 0;
+  __syncthreads();
   for (int j0 = 0; j0 < A.nblk; j0 += kWarps * 32) {
     const int j = j0 + warp * 32 + lane;
     const uint64_t key = j < A.nblk ? key_of(order_of(__ldcg(bm + j)), (uint32_t)j) : 0ull;
@@ -270,6 +289,93 @@ __device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift
       }
     }
   }
+  __syncthreads();
+}
+
+// Labels and log probabilities of the row's k best scores.  Every thread of
+// the CTA calls it.
+template <typename T>
+__device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift, int64_t b, double m, double logs,
+                                            SmemJ* S) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int k = A.k;
+  const float* bm = A.bmax + b * A.nblk;
+  // tau: the k-th best of the groups' best blocks is at most the k-th best block
+  if (A.nblk <= kGroups) {
+    if (tid < kGroups) S->gbest[tid] = tid < A.nblk ? key_of(order_of(__ldcg(bm + tid)), (uint32_t)tid) : 0ull;
+  } else {
+    const int grp = tid / (kThreads / kGroups);
+    uint64_t best = 0;
+    for (int j = grp + kGroups * (tid % (kThreads / kGroups)); j < A.nblk; j += kThreads) {
+      const uint64_t c = key_of(order_of(__ldcg(bm + j)), (uint32_t)j);
+      best = c > best ? c : best;
+    }
+    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
+    best = other > best ? other : best;
+    if (tid % 2 == 0) S->gbest[grp] = best;
+  }
+  if (tid == 0) { S->tau = 0; S->n = S->nb = 0; }
+  __syncthreads();
+  auto kth_group = [&] {                             // tau <- the k-th best of the groups
+    if (tid < kGroups) {
+      const uint64_t mine = S->gbest[tid];
+      int rank = 0;
+      for (int j = 0; j < kGroups; ++j) rank += S->gbest[j] > mine;
+      if (mine && rank == k - 1) S->tau = mine;
+    }
+    __syncthreads();
+  };
+  kth_group();
+  const uint64_t tau = S->tau;                       // 0: fewer than k blocks hold a score
+  // k scores are at least the score of tau's block
+  uint64_t floor_key = tau & 0xFFFFFFFF00000000ull;
+  if (tau == 0) {                                    // few blocks: groups of pairs of threads, a thread's best score
+    uint64_t best = 0;
+    for (int64_t blk = warp; blk < A.nblk; blk += kWarps) {
+      if (order_of(__ldcg(bm + blk)) == 0) continue;
+      float v[32];
+      load_block(z, A.L, shift, blk, lane, v);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
+        best = c > best ? c : best;
+      }
+    }
+    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
+    best = other > best ? other : best;
+    if (tid % 2 == 0) S->gbest[tid / 2] = best;
+    __syncthreads();
+    kth_group();
+    floor_key = S->tau;
+  }
+  // the blocks from tau's up, then their scores from the floor up
+  for (int j = tid; j < A.nblk; j += kThreads) {
+    const uint64_t key = key_of(order_of(__ldcg(bm + j)), (uint32_t)j);
+    if (key >= tau && key != 0) {
+      const int at = atomicAdd(&S->nb, 1);
+      if (at < kList) S->blocks[at] = j;
+    }
+  }
+  __syncthreads();
+  const int nb = S->nb;
+  if (nb <= kList) {
+    for (int j = warp; j < nb; j += kWarps) {
+      const int64_t blk = S->blocks[j];
+      float v[32];
+      load_block(z, A.L, shift, blk, lane, v);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        if (order_of(v[e]) < (uint32_t)(floor_key >> 32)) continue;
+        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
+        if (c != 0 && c >= floor_key) {
+          const int at = atomicAdd(&S->n, 1);
+          if (at < kCand) S->cand[at] = c;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (nb > kList || S->n > kCand) best_of_many(A, z, shift, b, tau, floor_key, S);   // ties, or scores in order
   __syncthreads();
   const int n = S->n;
   auto put = [&](int rank, uint64_t c) {
@@ -558,9 +664,9 @@ cudaError_t launch_score_logprobs(const void* Z, bool bf16, int64_t ldz, int32_t
   A.bmax = static_cast<float*>(work);
   A.part = reinterpret_cast<Stat*>(static_cast<char*>(work) + align256(sizeof(float) * (size_t)B * A.nblk));
   const int sms = current_sms();
-  // about 32 CTAs an SM, so that the last ones to end leave little idle, of at
-  // least a block a warp
-  int64_t per = ((int64_t)A.nblk * B + (int64_t)sms * 32 - 1) / ((int64_t)sms * 32);
+  // about 32 CTAs an SM, so that the last ones to end leave little idle, of
+  // whole rounds of a block a warp
+  int64_t per = ((int64_t)A.nblk * B / ((int64_t)sms * 32) + kWarps - 1) / kWarps * kWarps;
   if (per < kWarps) per = kWarps;
   int64_t splits = (A.nblk + per - 1) / per;
   if (splits > kMaxSplit) splits = kMaxSplit;

@@ -77,11 +77,19 @@ struct Soft {
 
   // 32 values with the maximum mx.  kMasks: values of -inf are ordinary (they
   // are cut at the floor, where e^ is 0); else they are rare, and a product 0
-  // times infinity sends the 32 values through the sums again.
+  // times infinity sends the 32 values through the sums again (add32_slow).
   template <bool kMasks>
   __device__ __forceinline__ void add32(const float (&v)[32], float mx) {
     if (mx > m) raise(mx);
     const float m0 = m > -INFINITY ? m : 0.0f;
+    float ss, tt;
+    sums32<kMasks>(v, m0, ss, tt);
+    if (!kMasks && tt != tt) slow32(v, m0, ss, tt);
+    s += ss;
+    t += tt;
+  }
+  template <bool kMasks>
+  __device__ __forceinline__ void sums32(const float (&v)[32], float m0, float& ss, float& tt) const {
     const f2 nm = pair(-m0, -m0), cc = pair(c2, c2);
     f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
@@ -100,29 +108,28 @@ struct Soft {
     float s0, s1, t0, t1;
     unpair(add2(ps[0], ps[1]), s0, s1);
     unpair(add2(pt[0], pt[1]), t0, t1);
-    float tt = t0 + t1;
-    if (!kMasks && tt != tt) {
-      tt = 0.0f;
+    ss = s0 + s1;
+    tt = t0 + t1;
+  }
+  __device__ __forceinline__ void slow32(const float (&v)[32], float m0, float& ss, float& tt) const {
+    ss = tt = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float d = max_nan(v[c] - m0, floor_v);
-        tt = fmaf(ex2(d * c2), d, tt);
-      }
+    for (int c = 0; c < 32; ++c) {
+      const float d = max_nan(v[c] - m0, floor_v), e = ex2(d * c2);
+      ss += e;
+      tt = fmaf(e, d, tt);
     }
-    s += s0 + s1;
-    t += tt;
   }
 
-  // another thread's sums; m of either may be -inf (nothing seen, or only NaN)
-  __device__ __forceinline__ void join(float om, float os, float ot) {
-    if (om > m) raise(om);
-    if (om == -INFINITY) {
-      s += os;
-      return;
+  // the warp's sums in every lane
+  __device__ __forceinline__ void join_warp() {
+    float mx = m;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    if (mx > m) raise(mx);
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
-    const float d = fmaxf(om - m, floor_v), c = om == m ? 1.0f : ex2(d * c2);
-    s = fmaf(os, c, s);
-    t = fmaf(c, om == m ? ot : fmaf(os, d, ot), t);
   }
 };
 
