@@ -32,7 +32,7 @@ using namespace tc;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = 1024;              // scores of a block
-constexpr int kMaxSplit = 512;
+constexpr int kMaxParts = 1024;           // CTAs of the pass
 
 // A score's place in the order as a whole number: larger is better, 0 for a
 // score that is never listed (-inf, NaN).  -0 and 0 are the same score.
@@ -40,6 +40,9 @@ __device__ __forceinline__ uint32_t order_of(float z) {
   if (!(z > -INFINITY)) return 0u;
   const uint32_t u = __float_as_uint(z + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float score_of(uint32_t order) {
+  return __uint_as_float((order & 0x80000000u) ? (order & 0x7FFFFFFFu) : ~order);
 }
 // (order, lower index first)
 __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
@@ -53,47 +56,44 @@ template <> __device__ __forceinline__ float score_at<uint16_t>(const uint16_t* 
 
 // Blocks are cut at 16-byte boundaries of the row's addresses: block j of a
 // row whose first score lies `shift` elements past such a boundary holds
-// scores [j kBlock - shift, (j + 1) kBlock - shift).  A thread has 32 of a
-// warp's 1024: kV vectors of 16 bytes.
+// scores [j kBlock - shift, (j + 1) kBlock - shift).  A lane of a warp has 32
+// of its 1024: kV vectors of 16 bytes.
 template <typename T> struct Vec { static constexpr int kE = 16 / sizeof(T); static constexpr int kV = 32 / kE; };
 
+// The 16 bytes of scores at, at + 1, ... of which some lie outside [0, L): -inf for those.
 template <typename T>
-__device__ __forceinline__ void load_block(const T* z, int64_t L, int shift, int64_t block, int lane, float (&v)[32]) {
-  constexpr int kE = Vec<T>::kE, kV = Vec<T>::kV;
-  const int64_t first = block * kBlock - shift;
-  if (first >= 0 && first + kBlock <= L) {
-    const uint4* p = reinterpret_cast<const uint4*>(z + first) + lane;
-    uint4 q[kV];
+__device__ __noinline__ uint4 ragged_vector(const T* z, int64_t L, int64_t at) {
+  uint32_t w[4];
+  auto bits = [&](int64_t l) -> uint32_t {
+    const uint32_t b = __float_as_uint(l < 0 || l >= L ? -INFINITY : score_at(z, l));
+    return sizeof(T) == 4 ? b : b >> 16;
+  };
 #pragma unroll
-    for (int i = 0; i < kV; ++i) q[i] = __ldg(p + 32 * i);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (sizeof(T) == 4) {
-          v[4 * i + e] = __uint_as_float(w[e]);
-        } else {
-          v[kE * i + 2 * e] = __uint_as_float(w[e] << 16);
-          v[kE * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const int64_t at = first + (32 * i + lane) * kE + e;
-        v[kE * i + e] = at >= 0 && at < L ? score_at(z, at) : -INFINITY;
-      }
-  }
+  for (int e = 0; e < 4; ++e) w[e] = sizeof(T) == 4 ? bits(at + e) : bits(at + 2 * e) | (bits(at + 2 * e + 1) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// the score's label of element e of load_block
+
 template <typename T>
-__device__ __forceinline__ int64_t label_of(int shift, int64_t block, int lane, int e) {
-  constexpr int kE = Vec<T>::kE;
-  return block * kBlock - shift + (32 * (e / kE) + lane) * kE + e % kE;
+__device__ __forceinline__ uint4 load_vector(const T* z, int64_t L, int64_t at) {
+  if (at >= 0 && at + Vec<T>::kE <= L) return __ldg(reinterpret_cast<const uint4*>(z + at));
+  return ragged_vector(z, L, at);
+}
+
+// Calls f(label, score) for the scores of a lane's i-th vector of a block, -inf for those that are none.
+template <typename T, typename F>
+__device__ __forceinline__ void visit_vector(const T* z, int64_t L, int shift, int64_t block, int i, int lane, F f) {
+  const int64_t at = block * kBlock - shift + (32 * i + lane) * Vec<T>::kE;
+  const uint4 q = load_vector(z, L, at);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (sizeof(T) == 4) {
+      f(at + e, __uint_as_float(w[e]));
+    } else {
+      f(at + 2 * e, __uint_as_float(w[e] << 16));
+      f(at + 2 * e + 1, __uint_as_float(w[e] & 0xFFFF0000u));
+    }
+  }
 }
 
 template <typename T> __host__ __device__ __forceinline__ int shift_of(const T* row) {
@@ -103,12 +103,12 @@ template <typename T> __host__ __device__ __forceinline__ int shift_of(const T* 
 struct Args {
   const void* Z;
   int64_t ldz, L;
-  int32_t B, k, nnz, splits, nblk;
+  int32_t B, k, nnz, nblk, parts;
   const int32_t *rowptr, *cols;
   float *logp, *lse, *entropy, *top_logp;
   int32_t* top_idx;
   float* bmax;            // [B][nblk] block maxima
-  Stat* part;             // [B][splits]
+  Stat* part;             // [parts + B] sums of each part of a row
 };
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -122,35 +122,57 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Adds a thread's 32 scores of a block to its sums; returns their maximum.
+// two bf16 numbers less an fp32 one
+__device__ __forceinline__ f2 minus_f32(uint32_t w, float m) {
+  float a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %3;\n\tadd.rn.f32.bf16 %1, h, %3;\n\t}"
+      : "=f"(a), "=f"(b) : "r"(w), "f"(-m));
+  return pair(a, b);
+}
+
+// A lane's 32 scores of a block as they are stored.
+template <typename T> struct Raw { uint4 q[Vec<T>::kV]; };
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* z, int64_t L, int64_t first, int lane) {
+  Raw<T> r;
+  if (first >= 0 && first + kBlock <= L) {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kV; ++i) r.q[i] = __ldg(reinterpret_cast<const uint4*>(z + first) + 32 * i + lane);
+  } else {                                             // a row's first or last block
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kV; ++i) r.q[i] = load_vector(z, L, first + (32 * i + lane) * Vec<T>::kE);
+  }
+  return r;
+}
+
+// Adds a lane's 32 scores to its sums; returns their maximum.
 //
-// bf16: two scores an instruction as far as that goes, or the issue slots bind
-// (256 rows of 500K: 70 us with seven and more a score, 56 with five and a half):
-// the maximum of the pairs, and -inf raised to the lowest finite number, whose
-// e^ is 0 and whose product with 0 is 0.  Where that number itself may be the
-// row's maximum, and on infinities and NaN, the sums are formed one by one.
-__device__ __forceinline__ float add_block(Soft& soft, const float* z, int64_t L, int shift, int64_t blk, int lane) {
+// bf16: two scores an instruction as far as that goes, or the issue slots
+// bind: the maximum of the pairs, and -inf raised to the lowest finite number,
+// whose e^ is 0 and whose product with 0 is 0.  Where that number itself may be
+// the row's maximum, and on infinities and NaN, the sums are formed one by one.
+__device__ __forceinline__ float add_raw(Soft& soft, const Raw<float>& r) {
   float v[32];
-  load_block(z, L, shift, blk, lane, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[4 * i] = __uint_as_float(r.q[i].x);
+    v[4 * i + 1] = __uint_as_float(r.q[i].y);
+    v[4 * i + 2] = __uint_as_float(r.q[i].z);
+    v[4 * i + 3] = __uint_as_float(r.q[i].w);
+  }
   const float mx = max32(v);
   soft.add32<true>(v, mx);
   return mx;
 }
-__device__ __forceinline__ float add_block(Soft& soft, const uint16_t* z, int64_t L, int shift, int64_t blk, int lane) {
-  const int64_t first = blk * kBlock - shift;
-  float v[32];
-  if (first < 0 || first + kBlock > L) {
-    load_block(z, L, shift, blk, lane, v);
-    const float mx = max32(v);
-    soft.add32<true>(v, mx);
-    return mx;
-  }
-  const uint4* p = reinterpret_cast<const uint4*>(z + first) + lane;
+__device__ __forceinline__ float add_raw(Soft& soft, const Raw<uint16_t>& r) {
   uint32_t w[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 q = __ldg(p + 32 * i);
-    w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+    w[4 * i] = r.q[i].x;
+    w[4 * i + 1] = r.q[i].y;
+    w[4 * i + 2] = r.q[i].z;
+    w[4 * i + 3] = r.q[i].w;
   }
   uint32_t x[4];
 #pragma unroll
@@ -161,14 +183,9 @@ __device__ __forceinline__ float add_block(Soft& soft, const uint16_t* z, int64_
   if (mx > soft.m) soft.raise(mx);
   const float m0 = soft.m > -INFINITY ? soft.m : 0.0f;
   float ss, tt;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t u = max_nan_bf16x2(w[i], 0xFF7FFF7Fu);
-    v[2 * i] = __uint_as_float(u << 16);
-    v[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
-  }
-  soft.sums32<false>(v, m0, ss, tt);
+  soft.sums32_of([&](int c) { return minus_f32(max_nan_bf16x2(w[c], 0xFF7FFF7Fu), m0); }, ss, tt);
   if (tt != tt || m0 < -1.0e38f) {
+    float v[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       v[2 * i] = __uint_as_float(w[i] << 16);
@@ -181,56 +198,76 @@ __device__ __forceinline__ float add_block(Soft& soft, const uint16_t* z, int64_
   return mx;
 }
 
-// The pass over a part of a row: the CTA's warps take its blocks in turn.
-// HBM-bound: every score is read once, in 16-byte loads, 128 (fp32) or 64
-// (bf16) bytes of a thread in flight.
-template <typename T>
-__device__ __forceinline__ Stat scan_row(const Args& A, const T* z, int shift, int64_t b, int64_t blk0, int64_t blk1,
-                                         Stat* red) {
+// The CTA's pass over blocks [blk0, blk1) of a row: the sums (in every thread)
+// and, for the list, the maxima of the blocks.  Warps take the blocks in
+// turn (not from a counter: the sums would depend on who came first).
+// HBM-bound: every score is read once, in 16-byte loads, the next block's 128
+// (fp32) or 64 (bf16) bytes of a lane in flight while this one's are added.
+template <int kW> struct SmemS { Stat row[kW]; };
+
+template <int kW, typename T>
+__device__ __forceinline__ Stat scan_blocks(const Args& A, const T* z, int64_t b, int blk0, int blk1, SmemS<kW>* S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shift = shift_of(z);
   Soft soft(1.0f);
-  for (int64_t blk = blk0 + warp; blk < blk1; blk += kWarps) {
-    float bm = add_block(soft, z, A.L, shift, blk, lane);
+  Raw<T> next;
+  int blk = blk0 + warp;
+  if (blk < blk1) next = load_raw(z, A.L, (int64_t)blk * kBlock - shift, lane);
+  while (blk < blk1) {
+    const Raw<T> now = next;
+    const int then = blk + kW;
+    if (then < blk1) next = load_raw(z, A.L, (int64_t)then * kBlock - shift, lane);
+    float bm = add_raw(soft, now);
     if (A.k > 0) {
       for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
       if (lane == 0) A.bmax[b * A.nblk + blk] = bm;
     }
+    blk = then;
   }
   soft.join_warp();
-  if (lane == 0) red[warp] = {soft.m, soft.s, soft.t};
+  __syncthreads();                                     // the last segment's sums are read
+  if (lane == 0) S->row[warp] = {soft.m, soft.s, soft.t};
   __syncthreads();
-  const Stat q = red[lane % kWarps];
   Soft all(1.0f);
-  if (lane < kWarps) { all.m = q.m; all.s = q.s; all.t = q.t; }
+  if (lane < kW) { all.m = S->row[lane].m; all.s = S->row[lane].s; all.t = S->row[lane].t; }
   all.join_warp();
   return {all.m, all.s, all.t};
 }
 
+// All rows' blocks are one run, cut into equal parts for the CTAs that the
+// machine holds: a part may cross rows, and its sums of row b go to slot
+// part + b, which no other part has and which keeps a row's slots together.
+__device__ __forceinline__ int64_t part_of(int64_t block, int64_t blocks, int64_t parts) {
+  return ((block + 1) * parts - 1) / blocks;
+}
+
 // ---------------------------------------------------------------- the row's answers
-constexpr int kGroups = 128;              // a lower bound on the k-th best block comes from the groups' best
-constexpr int kCand = 4096;               // keys the selection holds
-constexpr int kList = 512;                // blocks that may hold them
-constexpr int kBatch = kThreads * 8;      // keys added between two looks at the room
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kGroups = 128;              // groups of blocks, whose best bound the k-th best block from below
+constexpr int kHold = 8;                  // block maxima that a thread keeps
+constexpr int kCand = 4096;               // scores that the selection holds
+constexpr int kList = 512;                // blocks that may hold the k best
 
 struct SmemJ {
   uint64_t cand[kCand];
-  uint64_t gbest[kGroups];
-  uint64_t tau;
+  alignas(16) uint32_t gbest[kGroups];
+  uint32_t tau;
   int32_t blocks[kList];
   int n, nb;
-  double red[3 * kWarps];
-  Stat row[kWarps];
+  double red[2 * kJoinWarps];
+  float m[kJoinWarps];
 };
 
 // The keys cand[0 .. n) into descending order (n <= kCand), the rest zero.
 __device__ __forceinline__ void sort_desc(uint64_t* cand, int n) {
   int size2 = 1;
   while (size2 < n) size2 <<= 1;
-  for (int i = n + threadIdx.x; i < size2; i += kThreads) cand[i] = 0;
+  for (int i = n + threadIdx.x; i < size2; i += kJoinThreads) cand[i] = 0;
   __syncthreads();
   for (int size = 2; size <= size2; size <<= 1) {
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = threadIdx.x; i < size2 / 2; i += kThreads) {
+      for (int i = threadIdx.x; i < size2 / 2; i += kJoinThreads) {
         const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
         const uint64_t a = cand[lo], c = cand[hi];
         if ((a < c) == ((lo & size) == 0)) { cand[lo] = c; cand[hi] = a; }
@@ -240,56 +277,67 @@ __device__ __forceinline__ void sort_desc(uint64_t* cand, int n) {
   }
 }
 
-// The scores from floor_key up of the blocks from tau up, where they are more
-// than fit: in batches, of which the k best stay.
+// The k best of the blocks whose maximum has at least order tau, where the
+// blocks or their scores are more than fit: a block at a time, and the k best
+// stay when the room runs out.
 template <typename T>
-__device__ __noinline__ void best_of_many(const Args& A, const T* z, int shift, int64_t b, uint64_t tau,
-                                          uint64_t floor_key, SmemJ* S) {
+__device__ __noinline__ void best_of_many(const Args& A, const T* z, int shift, int64_t b, uint32_t tau, SmemJ* S) {
+  constexpr int kV = Vec<T>::kV;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int k = A.k;
   const float* bm = A.bmax + b * A.nblk;
+  uint64_t floor_key = (uint64_t)tau << 32;
   __syncthreads();
   if (tid == 0) S->n = 0;
-  __syncthreads();
-  for (int j0 = 0; j0 < A.nblk; j0 += kWarps * 32) {
-    const int j = j0 + warp * 32 + lane;
-    const uint64_t key = j < A.nblk ? key_of(order_of(__ldcg(bm + j)), (uint32_t)j) : 0ull;
-    uint32_t todo = __ballot_sync(0xFFFFFFFFu, key >= tau && key != 0);
-    // every warp goes round as often as the one with most blocks
-    while (__syncthreads_or(todo != 0)) {
-      float v[32];
-      int64_t blk = 0;
-      const bool on = todo != 0;
-      if (on) {
-        blk = j0 + warp * 32 + (__ffs((int)todo) - 1);
-        todo &= todo - 1;
-        load_block(z, A.L, shift, blk, lane, v);
-      }
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {                  // 8 scores of a thread at a time: at most 2048 keys
-        if (on) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = q == 0 ? v[e] : q == 1 ? v[8 + e] : q == 2 ? v[16 + e] : v[24 + e];
-            const uint64_t c = key_of(order_of(x), (uint32_t)label_of<T>(shift, blk, lane, 8 * q + e));
-            if (c != 0 && c >= floor_key) {
-              const int at = atomicAdd(&S->n, 1);
-              S->cand[at] = c;
-            }
-          }
-        }
+  for (int j0 = 0; j0 < A.nblk; j0 += kJoinThreads) {
+    __syncthreads();
+    if (tid == 0) S->nb = 0;
+    __syncthreads();
+    const uint32_t o = j0 + tid < A.nblk ? order_of(__ldcg(bm + j0 + tid)) : 0u;
+    if (o >= tau && o != 0) S->blocks[atomicAdd(&S->nb, 1)] = j0 + tid;
+    __syncthreads();
+    const int nb = S->nb;
+    for (int i = 0; i < nb; ++i) {
+      for (int v = warp; v < kV; v += kJoinWarps)
+        visit_vector(z, A.L, shift, S->blocks[i], v, lane, [&](int64_t l, float x) {
+          const uint64_t c = key_of(order_of(x), (uint32_t)l);
+          if (c != 0 && c >= floor_key) S->cand[atomicAdd(&S->n, 1)] = c;
+        });
+      __syncthreads();
+      const int n = S->n;                              // read by all before any thread adds to it again
+      if (__syncthreads_or(n > kCand - kBlock)) {
+        sort_desc(S->cand, n);
+        if (tid == 0) S->n = n < k ? n : k;
+        if (n >= k && S->cand[k - 1] > floor_key) floor_key = S->cand[k - 1];
         __syncthreads();
-        const int n = S->n;                          // read by all before any thread adds to it again
-        if (__syncthreads_or(n > kCand - kBatch)) {  // no room for another batch: keep the k best
-          sort_desc(S->cand, n);
-          if (tid == 0) S->n = n < k ? n : k;
-          if (n >= k && S->cand[k - 1] > floor_key) floor_key = S->cand[k - 1];
-          __syncthreads();
-        }
       }
     }
   }
   __syncthreads();
+}
+
+// tau <- the k-th best order of groups of neighbouring threads (0: fewer than
+// k hold a score), each thread's best given.
+__device__ __forceinline__ uint32_t kth_of_groups(uint32_t best, int k, SmemJ* S) {
+  constexpr int kPer = kJoinThreads / kGroups;
+  const int tid = threadIdx.x;
+  for (int o = 1; o < kPer; o <<= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  __syncthreads();
+  if (tid % kPer == 0) S->gbest[tid / kPer] = best;
+  if (tid == 0) S->tau = 0;
+  __syncthreads();
+  if (tid < kGroups) {
+    const uint32_t mine = S->gbest[tid];
+    int above = 0, same = 0;
+    for (int j = 0; j < kGroups; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(S->gbest + j);
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      same += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+    }
+    if (above < k && above + same >= k) S->tau = mine;
+  }
+  __syncthreads();
+  return S->tau;
 }
 
 // Labels and log probabilities of the row's k best scores.  Every thread of
@@ -297,93 +345,64 @@ __device__ __noinline__ void best_of_many(const Args& A, const T* z, int shift, 
 template <typename T>
 __device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift, int64_t b, double m, double logs,
                                             SmemJ* S) {
+  constexpr int kV = Vec<T>::kV;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int k = A.k;
   const float* bm = A.bmax + b * A.nblk;
-  // tau: the k-th best of the groups' best blocks is at most the k-th best block
-  if (A.nblk <= kGroups) {
-    if (tid < kGroups) S->gbest[tid] = tid < A.nblk ? key_of(order_of(__ldcg(bm + tid)), (uint32_t)tid) : 0ull;
-  } else {
-    const int grp = tid / (kThreads / kGroups);
-    uint64_t best = 0;
-    for (int j = grp + kGroups * (tid % (kThreads / kGroups)); j < A.nblk; j += kThreads) {
-      const uint64_t c = key_of(order_of(__ldcg(bm + j)), (uint32_t)j);
-      best = c > best ? c : best;
-    }
-    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
-    best = other > best ? other : best;
-    if (tid % 2 == 0) S->gbest[grp] = best;
-  }
-  if (tid == 0) { S->tau = 0; S->n = S->nb = 0; }
-  __syncthreads();
-  auto kth_group = [&] {                             // tau <- the k-th best of the groups
-    if (tid < kGroups) {
-      const uint64_t mine = S->gbest[tid];
-      int rank = 0;
-      for (int j = 0; j < kGroups; ++j) rank += S->gbest[j] > mine;
-      if (mine && rank == k - 1) S->tau = mine;
-    }
-    __syncthreads();
-  };
-  kth_group();
-  const uint64_t tau = S->tau;                       // 0: fewer than k blocks hold a score
-  // k scores are at least the score of tau's block
-  uint64_t floor_key = tau & 0xFFFFFFFF00000000ull;
-  if (tau == 0) {                                    // few blocks: groups of pairs of threads, a thread's best score
-    uint64_t best = 0;
-    for (int64_t blk = warp; blk < A.nblk; blk += kWarps) {
-      if (order_of(__ldcg(bm + blk)) == 0) continue;
-      float v[32];
-      load_block(z, A.L, shift, blk, lane, v);
+  // the blocks' orders, the first kHold of a thread kept
+  uint32_t held[kHold], best = 0;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
-        best = c > best ? c : best;
-      }
-    }
-    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, 1);
-    best = other > best ? other : best;
-    if (tid % 2 == 0) S->gbest[tid / 2] = best;
-    __syncthreads();
-    kth_group();
-    floor_key = S->tau;
+  for (int i = 0; i < kHold; ++i) {
+    const int j = tid + i * kJoinThreads;
+    held[i] = j < A.nblk ? order_of(__ldcg(bm + j)) : 0u;
   }
-  // the blocks from tau's up, then their scores from the floor up
-  for (int j = tid; j < A.nblk; j += kThreads) {
-    const uint64_t key = key_of(order_of(__ldcg(bm + j)), (uint32_t)j);
-    if (key >= tau && key != 0) {
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) best = max(best, held[i]);
+  for (int j = tid + kHold * kJoinThreads; j < A.nblk; j += kJoinThreads) best = max(best, order_of(__ldcg(bm + j)));
+  if (tid == 0) S->n = S->nb = 0;
+  // the k-th best of the groups' best is at most the k-th best block's
+  uint32_t tau = kth_of_groups(best, k, S);
+  auto list = [&](int j, uint32_t o) {
+    if (o >= tau && o != 0) {
       const int at = atomicAdd(&S->nb, 1);
       if (at < kList) S->blocks[at] = j;
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) list(tid + i * kJoinThreads, held[i]);
+  for (int j = tid + kHold * kJoinThreads; j < A.nblk; j += kJoinThreads) list(j, order_of(__ldcg(bm + j)));
   __syncthreads();
   const int nb = S->nb;
-  if (nb <= kList) {
-    for (int j = warp; j < nb; j += kWarps) {
-      const int64_t blk = S->blocks[j];
-      float v[32];
-      load_block(z, A.L, shift, blk, lane, v);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        if (order_of(v[e]) < (uint32_t)(floor_key >> 32)) continue;
-        const uint64_t c = key_of(order_of(v[e]), (uint32_t)label_of<T>(shift, blk, lane, e));
-        if (c != 0 && c >= floor_key) {
+  bool fits = nb <= kList;
+  if (tau == 0 && fits) {                              // few blocks: the threads' best scores in their place
+    best = 0;
+#pragma unroll 2
+    for (int it = warp; it < nb * kV; it += kJoinWarps)
+      visit_vector(z, A.L, shift, S->blocks[it / kV], it % kV, lane,
+                   [&](int64_t, float x) { best = max(best, order_of(x)); });
+    tau = kth_of_groups(best, k, S);
+  }
+  if (fits) {                                          // k scores have at least order tau
+#pragma unroll 2
+    for (int it = warp; it < nb * kV; it += kJoinWarps) {
+      visit_vector(z, A.L, shift, S->blocks[it / kV], it % kV, lane, [&](int64_t l, float x) {
+        const uint32_t o = order_of(x);
+        if (o >= tau && o != 0) {
           const int at = atomicAdd(&S->n, 1);
-          if (at < kCand) S->cand[at] = c;
+          if (at < kCand) S->cand[at] = key_of(o, (uint32_t)l);
         }
-      }
+      });
     }
     __syncthreads();
+    fits = S->n <= kCand;
   }
-  if (nb > kList || S->n > kCand) best_of_many(A, z, shift, b, tau, floor_key, S);   // ties, or scores in order
-  __syncthreads();
+  if (!fits) best_of_many(A, z, shift, b, tau, S);     // ties, or scores in order
   const int n = S->n;
   auto put = [&](int rank, uint64_t c) {
-    const int64_t l = index_of(c);
-    A.top_idx[b * k + rank] = (int32_t)l;
-    A.top_logp[b * k + rank] = (float)((double)score_at(z, l) - m - logs);
+    A.top_idx[b * k + rank] = (int32_t)index_of(c);
+    A.top_logp[b * k + rank] = (float)((double)score_of((uint32_t)(c >> 32)) - m - logs);
   };
-  if (n <= kThreads) {
+  if (n <= kJoinThreads) {
     if (tid < n) {
       const uint64_t mine = S->cand[tid];
       int rank = 0;
@@ -394,7 +413,7 @@ __device__ __forceinline__ void best_labels(const Args& A, const T* z, int shift
     sort_desc(S->cand, n);
     if (tid < k && tid < n) put(tid, S->cand[tid]);
   }
-  for (int r = n + tid; r < k; r += kThreads) {      // fewer scores than places
+  for (int r = n + tid; r < k; r += kJoinThreads) {    // fewer scores than places
     A.top_idx[b * k + r] = -1;
     A.top_logp[b * k + r] = -INFINITY;
   }
@@ -423,7 +442,7 @@ __device__ __forceinline__ void finish_row(const Args& A, const T* z, int shift,
   int e0 = A.rowptr[b], e1 = A.rowptr[b + 1];
   e0 = max(e0, 0);
   e1 = min(e1, A.nnz);
-  for (int e = e0 + tid; e < e1; e += kThreads) {
+  for (int e = e0 + tid; e < e1; e += kJoinThreads) {
     const int32_t l = A.cols[e];
     float r = NAN;
     if (l >= 0 && l < A.L) {
@@ -435,61 +454,75 @@ __device__ __forceinline__ void finish_row(const Args& A, const T* z, int shift,
   if (A.k > 0) best_labels(A, z, shift, b, mm, ll, S);
 }
 
+// The CTAs of the pass that an SM holds.
+template <typename T> constexpr int kResident = sizeof(T) == 4 ? 2 : 4;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) score_scan_kernel(const Args A) {
-  __shared__ Stat red[kWarps];
-  const int64_t b = blockIdx.y;
-  const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
+__global__ void __launch_bounds__(kThreads, kResident<T>) score_scan_kernel(const Args A) {
+  __shared__ SmemS<kWarps> S;
   pdl_trigger();
-  const int64_t n = A.nblk, i = blockIdx.x;
-  const Stat r = scan_row(A, z, shift_of(z), b, n * i / A.splits, n * (i + 1) / A.splits, red);
-  if (threadIdx.x == 0) A.part[b * A.splits + i] = r;
+  const int64_t w = blockIdx.x;
+  const int64_t N = (int64_t)A.B * A.nblk, end = N * (w + 1) / A.parts;
+  for (int64_t at = N * w / A.parts; at < end;) {
+    const int64_t b = at / A.nblk, stop = min(end, (b + 1) * A.nblk);
+    const Stat q = scan_blocks<kWarps>(A, static_cast<const T*>(A.Z) + b * A.ldz, b, (int)(at - b * A.nblk),
+                               (int)(stop - b * A.nblk), &S);
+    if (threadIdx.x == 0) A.part[w + b] = q;
+    at = stop;
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) score_join_kernel(const Args A) {
+__global__ void __launch_bounds__(kJoinThreads) score_join_kernel(const Args A) {
   __shared__ SmemJ S;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t b = blockIdx.x;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
-  const Stat* part = A.part + b * A.splits;
+  const int64_t N = (int64_t)A.B * A.nblk;
+  const int64_t w0 = part_of(b * A.nblk, N, A.parts), w1 = part_of((b + 1) * A.nblk - 1, N, A.parts);
+  const Stat* part = A.part + w0 + b;
+  const int n = (int)(w1 - w0 + 1);                    // at most kMaxParts: two of a thread
   pdl_wait();
+  Stat q[2];
   float mf = -INFINITY;
-  for (int i = tid; i < A.splits; i += kThreads) mf = fmaxf(mf, part[i].m);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    q[i] = tid + i * kJoinThreads < n ? part[tid + i * kJoinThreads] : Stat{-INFINITY, 0.0f, 0.0f};
+    mf = fmaxf(mf, q[i].m);
+  }
   for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xFFFFFFFFu, mf, o));
-  if (lane == 0) S.row[warp].m = mf;
+  if (lane == 0) S.m[warp] = mf;
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) mf = fmaxf(mf, S.row[w].m);
+  for (int w = 0; w < kJoinWarps; ++w) mf = fmaxf(mf, S.m[w]);
   const double m = mf;
   double s = 0.0, t = 0.0;
-  for (int i = tid; i < A.splits; i += kThreads) {
-    const Stat p = part[i];
-    if (p.m == -INFINITY) { s += p.s; continue; }
-    const double d = (double)p.m - m, c = p.m == mf ? 1.0 : exp(d);
-    s += c * p.s;
-    t += c * (p.t + (p.m == mf ? 0.0 : d * p.s));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (q[i].m == -INFINITY) { s += q[i].s; continue; }
+    const double d = (double)q[i].m - m, c = q[i].m == mf ? 1.0 : exp(d);
+    s += c * q[i].s;
+    t += c * (q[i].t + (q[i].m == mf ? 0.0 : d * q[i].s));
   }
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
   }
-  if (lane == 0) { S.red[warp] = s; S.red[kWarps + warp] = t; }
+  if (lane == 0) { S.red[warp] = s; S.red[kJoinWarps + warp] = t; }
   __syncthreads();
   s = t = 0.0;
-  for (int w = 0; w < kWarps; ++w) { s += S.red[w]; t += S.red[kWarps + w]; }
+  for (int w = 0; w < kJoinWarps; ++w) { s += S.red[w]; t += S.red[kJoinWarps + w]; }
   finish_row(A, z, shift_of(z), b, m, s, t, &S);
 }
 
 // Short rows: the pass and the answers in one CTA.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) score_row_kernel(const Args A) {
+__global__ void __launch_bounds__(kJoinThreads) score_row_kernel(const Args A) {
   __shared__ SmemJ S;
+  __shared__ SmemS<kJoinWarps> P;
   const int64_t b = blockIdx.x;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
-  const int shift = shift_of(z);
-  const Stat r = scan_row(A, z, shift, b, 0, A.nblk, S.row);
-  __syncthreads();
-  finish_row(A, z, shift, b, r.m, r.s, r.t, &S);
+  const Stat q = scan_blocks<kJoinWarps>(A, z, b, 0, A.nblk, &P);
+  finish_row(A, z, shift_of(z), b, q.m, q.s, q.t, &S);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -634,22 +667,28 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int32_t blocks_of(int64_t L) { return (int32_t)((L + 7 + kBlock - 1) / kBlock); }
 
 template <typename T>
-cudaError_t run_scores(const Args& A, cudaStream_t s) {
-  if (A.splits == 1) {
-    score_row_kernel<T><<<A.B, kThreads, 0, s>>>(A);
+cudaError_t run_scores(Args A, cudaStream_t s) {
+  // rows of up to two blocks a warp: one launch
+  if (A.nblk <= 2 * kJoinWarps) {
+    score_row_kernel<T><<<A.B, kJoinThreads, 0, s>>>(A);
     return cudaGetLastError();
   }
-  score_scan_kernel<T><<<dim3(A.splits, A.B), kThreads, 0, s>>>(A);
+  const int64_t N = (int64_t)A.B * A.nblk;
+  int64_t parts = (int64_t)current_sms() * kResident<T>;
+  if (parts > kMaxParts) parts = kMaxParts;
+  if (parts > N / kWarps) parts = N / kWarps;          // a block a warp at least
+  A.parts = (int32_t)parts;
+  score_scan_kernel<T><<<(unsigned)parts, kThreads, 0, s>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_after(score_join_kernel<T>, dim3(A.B), kThreads, 0, s, A);
+  return launch_after(score_join_kernel<T>, dim3(A.B), kJoinThreads, 0, s, A);
 }
 
 }  // namespace
 
 size_t score_logprobs_workspace(int32_t B, int64_t L, int32_t k) {
   (void)k;
-  return align256(sizeof(float) * (size_t)B * blocks_of(L)) + align256(sizeof(Stat) * (size_t)B * kMaxSplit);
+  return align256(sizeof(float) * (size_t)B * blocks_of(L)) + align256(sizeof(Stat) * ((size_t)B + kMaxParts));
 }
 
 cudaError_t launch_score_logprobs(const void* Z, bool bf16, int64_t ldz, int32_t B, int64_t L, const int32_t* rowptr,
@@ -663,15 +702,6 @@ cudaError_t launch_score_logprobs(const void* Z, bool bf16, int64_t ldz, int32_t
   A.nblk = blocks_of(L);
   A.bmax = static_cast<float*>(work);
   A.part = reinterpret_cast<Stat*>(static_cast<char*>(work) + align256(sizeof(float) * (size_t)B * A.nblk));
-  const int sms = current_sms();
-  // about 32 CTAs an SM, so that the last ones to end leave little idle, of
-  // whole rounds of a block a warp
-  int64_t per = ((int64_t)A.nblk * B / ((int64_t)sms * 32) + kWarps - 1) / kWarps * kWarps;
-  if (per < kWarps) per = kWarps;
-  int64_t splits = (A.nblk + per - 1) / per;
-  if (splits > kMaxSplit) splits = kMaxSplit;
-  if (A.nblk <= 4 * kWarps) splits = 1;
-  A.splits = (int32_t)splits;
   return bf16 ? run_scores<uint16_t>(A, s) : run_scores<float>(A, s);
 }
 

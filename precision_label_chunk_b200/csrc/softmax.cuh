@@ -90,16 +90,26 @@ struct Soft {
   }
   template <bool kMasks>
   __device__ __forceinline__ void sums32(const float (&v)[32], float m0, float& ss, float& tt) const {
-    const f2 nm = pair(-m0, -m0), cc = pair(c2, c2);
-    f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    const f2 nm = pair(-m0, -m0);
+    sums32_of([&](int c) {
       f2 d = add2(pair(v[2 * c], v[2 * c + 1]), nm);
-      float a, b;
       if (kMasks) {
+        float a, b;
         unpair(d, a, b);
         d = pair(max_nan(a, floor_v), max_nan(b, floor_v));
       }
+      return d;
+    }, ss, tt);
+  }
+  // sums over the 16 pairs of differences v - m that diff(c) gives
+  template <typename F>
+  __device__ __forceinline__ void sums32_of(F diff, float& ss, float& tt) const {
+    const f2 cc = pair(c2, c2);
+    f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const f2 d = diff(c);
+      float a, b;
       unpair(mul2(d, cc), a, b);
       const f2 e = pair(ex2(a), ex2(b));
       ps[c & 1] = add2(ps[c & 1], e);
