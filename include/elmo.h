@@ -468,7 +468,7 @@ elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_
  *
  *   codes_dev, scales_dev, L, d, group : as in elmo_q4_pack.
  *   X_dev : bf16 [B x d], 1 <= B <= ELMO_MAX_PREDICT_BATCH.  Batches are taken
- *           32 queries (fewer for d above 1024) to a pass over the codes.
+ *           32 queries (fewer for wide heads) to a pass over the codes.
  *   Z_dev : fp32, row b at Z_dev + b * ldz, ldz >= L; entries [L, ldz) of a
  *           row are left as they are.
  * A wait that ran out leaves NaN in the scores it could not form.

@@ -216,6 +216,14 @@ __device__ __forceinline__ void q4_pairs(uint32_t c, uint32_t (&p)[4]) {
   }
 }
 
+// d = a b, and d += a b
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -235,6 +243,12 @@ struct SmemQ {
   int32_t exponent[8 * kQMaxNB];
   int abort;
 };
+
+// Shared memory beside the ring: X's fragments, two tiles of scales.
+template <int kMT, int kNB, int kWarps>
+size_t q4_fixed(int d, int group) {
+  return 1024 + (size_t)d * kNB * 16 + (size_t)4 * 16 * kMT * kWarps * (d / group) + sizeof(SmemQ);
+}
 
 struct Q4Args {
   const uint16_t* scales;
@@ -277,14 +291,15 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
   if (warp == kWarps) {
     if (elect_one()) {
       tma_prefetch_desc(&tmQ);
-      uint32_t it = 0;
+      uint32_t s = 0, ph = 1;
       for (int64_t tile = blockIdx.x; tile < T && !*abort; tile += gridDim.x) {
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = (int)(it % (uint32_t)A.stages);
-          const uint32_t ph = (it / (uint32_t)A.stages) & 1;
-          if (!mbar_wait(&S->empty[s], ph ^ 1, abort, kQWait)) { *abort = 1; break; }
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&S->empty[s], ph, abort, kQWait)) { *abort = 1; break; }
           mbar_arrive_expect_tx(&S->full[s], kStage);
-          tma_load_2d(ring + (size_t)s * kStage, &tmQ, &S->full[s], kb * kQKB, (int32_t)(tile * kTile));
+          // boxes have at most 256 rows
+          for (int r = 0; r < kTile; r += 256)
+            tma_load_2d(ring + (size_t)s * kStage + (size_t)r * kQKB, &tmQ, &S->full[s], kb * kQKB, (int32_t)(tile * kTile + r));
+          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
         }
       }
     }
@@ -357,9 +372,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
     };
     if ((int64_t)blockIdx.x < T) fetch_scales(blockIdx.x, 0);
 
-    uint32_t it = 0;
+    constexpr int kGroupsStage = 2 * kQKB / kG;
+    uint32_t s = 0, ph = 0;
     int buf = 0;
     const int row0 = warp * kRows + q4_row<kG>(g);     // of the tile: fragment rows g, g + 8 are rows row0, row0 + 8
+    // byte t kG / 8 of a row's group j, swizzled; rows row0 + 8 i share row & 7
+    const uint32_t mine = smem_u32(ring) + (uint32_t)row0 * kQKB, swz = (uint32_t)(row0 & 7) << 4;
     for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x, buf ^= 1) {
       cp_async_wait();
       __syncwarp();
@@ -372,61 +390,64 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) out[m][nb][e] = 0.0f;
       const uint16_t* ts = sc + (size_t)buf * kTile * ng + (size_t)row0 * ng;
+      const uint4* xp = xs + lane;
       bool ok = true;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = (int)(it % (uint32_t)A.stages);
-        const uint32_t ph = (it / (uint32_t)A.stages) & 1;
-        if (!mbar_wait(&S->full[s], ph, abort, kQWait)) { *abort = 1; ok = false; break; }
-        const uint32_t st = smem_u32(ring) + (uint32_t)s * kStage + (uint32_t)row0 * kQKB;
-        const int j1 = min(2 * kQKB / kG, ng - kb * (2 * kQKB / kG));
-#pragma unroll 2
-        for (int j = 0; j < j1; ++j) {
-          const int gi = kb * (2 * kQKB / kG) + j;
-          float acc[kMT][kNB][4];
+      // one group: its sum in fp32, then times the labels' scales
+      auto group = [&](uint32_t st, int j) {
+        const uint32_t at = st + (((uint32_t)(j * (kG / 2) + t * (kG / 8))) ^ swz);
+        float acc[kMT][kNB][4];
+        uint32_t c[2 * kMT][kWords];
 #pragma unroll
-          for (int m = 0; m < kMT; ++m)
+        for (int r = 0; r < 2 * kMT; ++r) lds_words<kWords>(at + (uint32_t)(r * 8 * kQKB), c[r]);
+        float sl[kMT], sh[kMT];
 #pragma unroll
-            for (int nb = 0; nb < kNB; ++nb)
+        for (int m = 0; m < kMT; ++m) {
+          sl[m] = bf16_to_f32(ts[(size_t)(16 * m) * ng + j]);
+          sh[m] = bf16_to_f32(ts[(size_t)(16 * m + 8) * ng + j]);
+        }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[m][nb][e] = 0.0f;
-          const uint32_t byte = (uint32_t)(j * (kG / 2) + t * (kG / 8));
-          // rows row0 + 8 i share row & 7: the same swizzle
-          const uint32_t at = (((byte >> 4) ^ (uint32_t)(row0 & 7)) << 4) | (byte & 15u);
-          uint32_t c[2 * kMT][kWords];
+        for (int w = 0; w < kWords; ++w) {
+          uint4 x[kNB];
 #pragma unroll
-          for (int r = 0; r < 2 * kMT; ++r) lds_words<kWords>(st + at + (uint32_t)(r * 8 * kQKB), c[r]);
-#pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            uint4 x[kNB];
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb) x[nb] = xs[(((size_t)gi * kWords + w) * kNB + nb) * 32 + lane];
-#pragma unroll
-            for (int m = 0; m < kMT; ++m) {
-              uint32_t p[4], q[4];
-              q4_pairs(c[2 * m][w], p);
-              q4_pairs(c[2 * m + 1][w], q);
-#pragma unroll
-              for (int nb = 0; nb < kNB; ++nb) {
-                mma_f16(acc[m][nb], p[0], q[0], p[1], q[1], x[nb].x, x[nb].y);
-                mma_f16(acc[m][nb], p[2], q[2], p[3], q[3], x[nb].z, x[nb].w);
-              }
-            }
-          }
+          for (int nb = 0; nb < kNB; ++nb) x[nb] = xp[((j * kWords + w) * kNB + nb) * 32];
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
-            const float s0 = bf16_to_f32(ts[(size_t)(16 * m) * ng + gi]);
-            const float s1 = bf16_to_f32(ts[(size_t)(16 * m + 8) * ng + gi]);
+            uint32_t p[4], q[4];
+            q4_pairs(c[2 * m][w], p);
+            q4_pairs(c[2 * m + 1][w], q);
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
-              out[m][nb][0] = __fmaf_rn(s0, acc[m][nb][0], out[m][nb][0]);
-              out[m][nb][1] = __fmaf_rn(s0, acc[m][nb][1], out[m][nb][1]);
-              out[m][nb][2] = __fmaf_rn(s1, acc[m][nb][2], out[m][nb][2]);
-              out[m][nb][3] = __fmaf_rn(s1, acc[m][nb][3], out[m][nb][3]);
+              if (w == 0) mma_f16_zero(acc[m][nb], p[0], q[0], p[1], q[1], x[nb].x, x[nb].y);
+              else mma_f16(acc[m][nb], p[0], q[0], p[1], q[1], x[nb].x, x[nb].y);
+              mma_f16(acc[m][nb], p[2], q[2], p[3], q[3], x[nb].z, x[nb].w);
             }
           }
         }
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb) {
+            out[m][nb][0] = __fmaf_rn(sl[m], acc[m][nb][0], out[m][nb][0]);
+            out[m][nb][1] = __fmaf_rn(sl[m], acc[m][nb][1], out[m][nb][1]);
+            out[m][nb][2] = __fmaf_rn(sh[m], acc[m][nb][2], out[m][nb][2]);
+            out[m][nb][3] = __fmaf_rn(sh[m], acc[m][nb][3], out[m][nb][3]);
+          }
+      };
+      for (int left = ng; left > 0; left -= kGroupsStage) {
+        if (!mbar_wait(&S->full[s], ph, abort, kQWait)) { *abort = 1; ok = false; break; }
+        const uint32_t st = mine + s * kStage;
+        if (left >= kGroupsStage) {
+#pragma unroll
+          for (int j = 0; j < kGroupsStage; ++j) group(st, j);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < left; ++j) group(st, j);
+        }
+        ts += kGroupsStage;
+        xp += kGroupsStage * kWords * kNB * 32;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S->empty[s]);
+        if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
       }
       if (!ok) {        // a wait ran out: no score of the tiles left is valid
         for (int64_t tl = tile; tl < T; tl += gridDim.x)
@@ -466,35 +487,40 @@ template <int kG, int kMT, int kNB, int kWarps>
 cudaError_t run_q4(const uint8_t* codes, Q4Args A, int sms, cudaStream_t s) {
   constexpr int kTile = 16 * kMT * kWarps;
   constexpr size_t kStage = (size_t)kTile * kQKB;
-  const size_t fixed = 1024 + (size_t)(A.d / 8) * kNB * 128 + (size_t)4 * kTile * (A.d / kG) + sizeof(SmemQ);
-  int stages = (int)((kQSmem - fixed) / kStage);
+  const size_t fixed = q4_fixed<kMT, kNB, kWarps>(A.d, kG);
   const int64_t T = (A.L + kTile - 1) / kTile;
   const int64_t boxes = (A.d / 2 + kQKB - 1) / kQKB * ((T + sms - 1) / sms);
+  int stages = (int)((kQSmem - fixed) / kStage);
   if (stages > kQMaxStages) stages = kQMaxStages;
   if (stages > boxes) stages = (int)boxes;
   A.stages = stages;
-  const size_t smem = fixed + (size_t)stages * kStage;
   CUtensorMap tm;
-  cudaError_t e = make_tma_map_2d(&tm, codes, 1, (uint64_t)A.d / 2, (uint64_t)A.L, (uint64_t)A.d / 2, kTile);
+  cudaError_t e = make_tma_map_2d(&tm, codes, 1, (uint64_t)A.d / 2, (uint64_t)A.L, (uint64_t)A.d / 2,
+                                  kTile < 256 ? kTile : 256);
   if (e != cudaSuccess) return e;
   auto k = q4_scores_kernel<kG, kMT, kNB, kWarps>;
   static std::atomic<uint64_t> seen{0};
   if ((e = allow_smem(k, (int)kQSmem, seen)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(T < sms ? T : sms), (unsigned)((A.B + 8 * kNB - 1) / (8 * kNB)));
-  k<<<grid, 32 * (kWarps + 1), smem, s>>>(tm, A);
+  k<<<grid, 32 * (kWarps + 1), fixed + (size_t)stages * kStage, s>>>(tm, A);
   return cudaGetLastError();
+}
+
+template <int kMT, int kNB, int kWarps>
+bool q4_fits(int d, int group) {          // two stages at least
+  return q4_fixed<kMT, kNB, kWarps>(d, group) + (size_t)2 * 16 * kMT * kWarps * kQKB <= kQSmem;
 }
 
 template <int kG>
 cudaError_t run_q4_group(const uint8_t* codes, const Q4Args& A, cudaStream_t s) {
   const int sms = current_sms();
-  // queries of one pass over the codes: as many as the fragments of X leave room for
   const int nb = (A.B + 7) / 8;
-  const size_t x1 = (size_t)A.d * 16;                // X fragments of 8 queries
-  const int most = (int)((64 * 1024) / x1) < 1 ? 1 : (int)((64 * 1024) / x1);
-  const int want = nb < most ? nb : most;
-  if (want >= 4) return run_q4<kG, 1, 4, 8>(codes, A, sms, s);
-  if (want >= 2) return run_q4<kG, 1, 2, 8>(codes, A, sms, s);
+  // as many queries to a pass over the codes as there are, up to 32
+  if (nb > 2 && q4_fits<1, 4, 16>(A.d, kG)) return run_q4<kG, 1, 4, 16>(codes, A, sms, s);
+  if (nb > 1 && q4_fits<1, 2, 16>(A.d, kG)) return run_q4<kG, 1, 2, 16>(codes, A, sms, s);
+  // a few queries: two label blocks a warp share each read of X where there are tiles for every SM
+  if (A.L >= (int64_t)sms * 512 && q4_fits<2, 1, 16>(A.d, kG)) return run_q4<kG, 2, 1, 16>(codes, A, sms, s);
+  if (A.L >= (int64_t)sms * 256 && q4_fits<1, 1, 16>(A.d, kG)) return run_q4<kG, 1, 1, 16>(codes, A, sms, s);
   return run_q4<kG, 1, 1, 8>(codes, A, sms, s);
 }
 
