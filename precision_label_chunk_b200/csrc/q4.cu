@@ -200,14 +200,28 @@ template <> __device__ __forceinline__ void lds_words<4>(uint32_t addr, uint32_t
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
+// (a & mask) | magic in one instruction: of two constants the compiler makes
+// two instructions, which took the integer pipe to 63 % and the 3M-label query
+// from 286 us to what stands below, so the magic number comes in a register.
+__device__ __forceinline__ uint32_t mask_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+  return r;
+}
+__device__ __forceinline__ uint32_t q4_magic() {
+  uint32_t r;
+  asm("mov.b32 %0, 0x64006400;" : "=r"(r));
+  return r;
+}
+
 // 8 codes (elements 0..7, nibble i = element i) -> pairs (0,4), (1,5), (2,6), (3,7) of u - 8
-__device__ __forceinline__ void q4_pairs(uint32_t c, uint32_t (&p)[4]) {
+__device__ __forceinline__ void q4_pairs(uint32_t c, uint32_t magic, uint32_t (&p)[4]) {
   const uint32_t hi = c >> 8;
   const __half2 m1032 = __half2half2(__ushort_as_half(0x6408));          // 1032
   const __half2 r16 = __half2half2(__ushort_as_half(0x2C00));            // 1 / 16
   const __half2 m72 = __half2half2(__ushort_as_half(0xD480));            // -72
-  uint32_t w[4] = {(c & 0x000F000Fu) | 0x64006400u, (c & 0x00F000F0u) | 0x64006400u,
-                   (hi & 0x000F000Fu) | 0x64006400u, (hi & 0x00F000F0u) | 0x64006400u};
+  const uint32_t w[4] = {mask_or(c, 0x000F000Fu, magic), mask_or(c, 0x00F000F0u, magic),
+                         mask_or(hi, 0x000F000Fu, magic), mask_or(hi, 0x00F000F0u, magic)};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const __half2 v = *reinterpret_cast<const __half2*>(&w[e]);
@@ -238,11 +252,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
+// 2^e as two factors that are normal numbers (|e| <= 250)
+__device__ __forceinline__ void pow2_factors(int e, float& f0, float& f1) {
+  f0 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
+  f1 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
+}
+
 struct SmemQ {
   uint64_t full[kQMaxStages], empty[kQMaxStages];
   int32_t exponent[8 * kQMaxNB];
   int abort;
 };
+
+// Rows of a TMA box: at most 256.
+constexpr int q4_box(int tile) { return tile / ((tile + 255) / 256); }
 
 // Shared memory beside the ring: X's fragments, two tiles of scales.
 template <int kMT, int kNB, int kWarps>
@@ -267,6 +290,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
   constexpr int kRows = 16 * kMT;                    // labels of a warp
   constexpr int kTile = kRows * kWarps;              // labels of a tile
   constexpr uint32_t kStage = kTile * kQKB;
+  constexpr int kBox = q4_box(kTile);
   constexpr int kWords = kG / 32;                    // words of 8 codes a thread has of a group and row
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -296,8 +320,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(&S->empty[s], ph, abort, kQWait)) { *abort = 1; break; }
           mbar_arrive_expect_tx(&S->full[s], kStage);
-          // boxes have at most 256 rows
-          for (int r = 0; r < kTile; r += 256)
+          for (int r = 0; r < kTile; r += kBox)
             tma_load_2d(ring + (size_t)s * kStage + (size_t)r * kQKB, &tmQ, &S->full[s], kb * kQKB, (int32_t)(tile * kTile + r));
           if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1; }
         }
@@ -336,12 +359,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
         const int k = j * kG + (ln & 3) * (kG / 4) + 8 * w;
         const uint4 v = *reinterpret_cast<const uint4*>(A.X + (size_t)(b0 + n) * A.d + k);
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        const int e = S->exponent[n];
+        float f0, f1;
+        pow2_factors(S->exponent[n], f0, f1);
         __half h[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[2 * i] = __float2half_rn(ldexpf(__uint_as_float(x[i] << 16), e));
-          h[2 * i + 1] = __float2half_rn(ldexpf(__uint_as_float(x[i] & 0xFFFF0000u), e));
+          h[2 * i] = __float2half_rn(__uint_as_float(x[i] << 16) * f0 * f1);
+          h[2 * i + 1] = __float2half_rn(__uint_as_float(x[i] & 0xFFFF0000u) * f0 * f1);
         }
         uint32_t p[4];
 #pragma unroll
@@ -373,6 +397,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
     if ((int64_t)blockIdx.x < T) fetch_scales(blockIdx.x, 0);
 
     constexpr int kGroupsStage = 2 * kQKB / kG;
+    const uint32_t magic = q4_magic();
     uint32_t s = 0, ph = 0;
     int buf = 0;
     const int row0 = warp * kRows + q4_row<kG>(g);     // of the tile: fragment rows g, g + 8 are rows row0, row0 + 8
@@ -413,8 +438,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
             uint32_t p[4], q[4];
-            q4_pairs(c[2 * m][w], p);
-            q4_pairs(c[2 * m + 1][w], q);
+            q4_pairs(c[2 * m][w], magic, p);
+            q4_pairs(c[2 * m + 1][w], magic, q);
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
               if (w == 0) mma_f16_zero(acc[m][nb], p[0], q[0], p[1], q[1], x[nb].x, x[nb].y);
@@ -462,18 +487,15 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
         for (int c = 0; c < 2; ++c) {
           const int n = nb * 8 + 2 * t + c;
           if (b0 + n >= A.B) continue;
-          const int e = -S->exponent[n];
-          // 2^e in two factors, each a normal number
-          const float f0 = __uint_as_float((uint32_t)(127 + e / 2) << 23);
-          const float f1 = __uint_as_float((uint32_t)(127 + e - e / 2) << 23);
-          float* z = A.Z + (int64_t)(b0 + n) * A.ldz;
+          float f0, f1;
+          pow2_factors(-S->exponent[n], f0, f1);
+          float* z = A.Z + (int64_t)(b0 + n) * A.ldz + tile * kTile + row0;
+          const int64_t left = A.L - tile * kTile - row0;
 #pragma unroll
           for (int m = 0; m < kMT; ++m) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t l = tile * kTile + row0 + 16 * m + 8 * h;
-              if (l < A.L) __stcs(z + l, out[m][nb][2 * h + c] * f0 * f1);
-            }
+            for (int h = 0; h < 2; ++h)
+              if (16 * m + 8 * h < left) __stcs(z + 16 * m + 8 * h, out[m][nb][2 * h + c] * f0 * f1);
           }
         }
       }
@@ -496,7 +518,7 @@ cudaError_t run_q4(const uint8_t* codes, Q4Args A, int sms, cudaStream_t s) {
   A.stages = stages;
   CUtensorMap tm;
   cudaError_t e = make_tma_map_2d(&tm, codes, 1, (uint64_t)A.d / 2, (uint64_t)A.L, (uint64_t)A.d / 2,
-                                  kTile < 256 ? kTile : 256);
+                                  q4_box(kTile));
   if (e != cudaSuccess) return e;
   auto k = q4_scores_kernel<kG, kMT, kNB, kWarps>;
   static std::atomic<uint64_t> seen{0};
