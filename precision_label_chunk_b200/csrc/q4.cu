@@ -25,8 +25,8 @@ namespace {
 using namespace tc;
 
 // ---------------------------------------------------------------- pack, unpack
-// Rows are whole groups, so the matrix is one run of groups: a thread takes 16
-// consecutive weights, the G / 16 threads of a group share their maximum.
+// Rows are whole groups, so the matrix is one run of groups: a thread takes
+// eight consecutive weights, the G / 8 threads of a group share their maximum.
 //
 // w / s is rounded to the nearest whole number without a division: with
 // r = 1 / s to within a few units in the last place, t = w r is near w / s,
@@ -34,82 +34,108 @@ using namespace tc;
 // have 8-bit significands a 2^e and b 2^f; near k + 1/2 >= 1/2 they have
 // e >= f - 1, so w / s - (k + 1/2) is a multiple of 1 / (2 b)).  Rounding t to
 // a multiple of 2^-13 (the sum with 1.5 2^10) therefore restores exact ties
-// and moves nothing else across one, and the sum with 1.5 2^23 then rounds
-// ties to even.  Scales below 2^-100, whose reciprocal may overflow and whose
-// own rounding may be coarse, take the division.
+// and moves nothing else across one, and the sum that brings 1.5 2^23 + 8 into
+// its place then rounds ties to even and leaves the code in the low byte.
+// Likewise max / 7 rounds to bf16 as max times fl(1 / 7) does: 7 times a
+// midpoint of that grid has more bits than max, so max / 7 stays 1 / 14 of a
+// step away from every midpoint.  Scales below 2^-100, whose own rounding may
+// be coarse, take the division.
 //
-// HBM-bound: bytes of W, half a byte a weight, the scales.  Five fp32
-// operations a weight keep the arithmetic below the time of the bytes.
+// HBM-bound: the bytes of W, half a byte a weight, the scales.  A thread has
+// kPackAt vectors in flight, each warp access contiguous (16 weights a thread,
+// two vectors apart, measured 214 us for 500K bf16 labels x 768).
 constexpr int kPackThreads = 256;
+constexpr int kPackAt = 4;
+
+template <int kFormat> struct Raw8 { uint2 v; };
+template <> struct Raw8<ELMO_BF16> { uint4 v; };
 
 template <int kFormat>
-__device__ __forceinline__ void load16(const void* W, int64_t i, float (&w)[16]) {
-  if (kFormat == ELMO_BF16) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + i);
-    const uint4 a = __ldcs(p), b = __ldcs(p + 1);
-    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void values8(const Raw8<kFormat>& r, float (&w)[8]) {
+  if constexpr (kFormat == ELMO_BF16) {
+    const uint32_t v[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
       w[2 * e] = __uint_as_float(v[e] << 16);
       w[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
     }
   } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(W) + i));
-    const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+    float a[4], b[4];
+    if constexpr (kFormat == ELMO_FP8_E5M2) { e5m2x4_to_f32(r.v.x, a); e5m2x4_to_f32(r.v.y, b); }
+    else { e4m3x4_to_f32(r.v.x, a); e4m3x4_to_f32(r.v.y, b); }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float f[4];
-      if (kFormat == ELMO_FP8_E5M2) e5m2x4_to_f32(v[e], f);
-      else e4m3x4_to_f32(v[e], f);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) w[4 * e + q] = f[q];
-    }
+    for (int e = 0; e < 4; ++e) { w[e] = a[e]; w[4 + e] = b[e]; }
   }
 }
 
+// the largest magnitude's code of eight weights, and a code's value
+template <int kFormat> __device__ __forceinline__ uint32_t code_max(const Raw8<kFormat>& r) {
+  if constexpr (kFormat == ELMO_BF16) {
+    constexpr uint32_t k = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(r.v.x & k, r.v.y & k), __vmaxu2(r.v.z & k, r.v.w & k));
+    return max(m & 0xFFFFu, m >> 16);
+  } else {
+    constexpr uint32_t k = 0x7F007F00u;
+    const uint32_t m = __vmaxu2(__vmaxu2(r.v.x & k, (r.v.x << 8) & k), __vmaxu2(r.v.y & k, (r.v.y << 8) & k));
+    return max(m & 0xFFFFu, m >> 16) >> 8;
+  }
+}
+template <int kFormat> __device__ __forceinline__ float code_value(uint32_t m) {
+  if constexpr (kFormat == ELMO_BF16) return bf16_to_f32((uint16_t)m);
+  else if constexpr (kFormat == ELMO_FP8_E5M2) return e5m2_to_f32((uint8_t)m);
+  else return e4m3_to_f32((uint8_t)m);
+}
+
+// sum over e of 16^e times the bits of 1.5 2^23 (0x4B400000), mod 2^32
+constexpr uint32_t kCodeBits = 0x4B400000u * 0x11111111u;
+
 template <int kFormat>
-__global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const void* __restrict__ W, int64_t n16, int lanes,
-                                                               uint2* __restrict__ codes,
+__global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const Raw8<kFormat>* __restrict__ W, int64_t n8, int lanes,
+                                                               uint32_t* __restrict__ codes,
                                                                uint16_t* __restrict__ scales) {
   // every thread of a warp stays for the shuffles; groups never straddle warps
-  const int64_t stride = (int64_t)gridDim.x * kPackThreads;
-  for (int64_t i0 = (int64_t)blockIdx.x * kPackThreads; i0 < n16; i0 += stride) {
-    const int64_t i = i0 + threadIdx.x;
-    float w[16];
-    uint32_t m = 0;                                    // the magnitudes' bits order them, NaN above inf
-    if (i < n16) {
-      load16<kFormat>(W, i * 16, w);
+  const int64_t stride = (int64_t)gridDim.x * kPackThreads * kPackAt;
+  for (int64_t i0 = (int64_t)blockIdx.x * kPackThreads * kPackAt + threadIdx.x; i0 - threadIdx.x < n8; i0 += stride) {
+    Raw8<kFormat> raw[kPackAt];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) m = max(m, __float_as_uint(w[e]) & 0x7FFFFFFFu);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = 0.0f;
+    for (int u = 0; u < kPackAt; ++u) {
+      const int64_t i = i0 + u * kPackThreads;
+      if (i < n8) raw[u].v = __ldcs(&W[i].v);
+      else raw[u] = Raw8<kFormat>{};
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const bool finite = m < 0x7F800000u;
-    const uint16_t sb = finite ? f32_to_bf16_rn(__fdiv_rn(__uint_as_float(m), 7.0f)) : (uint16_t)0x7FC0u;
-    const float s = bf16_to_f32(sb);
-    uint32_t q[2] = {0u, 0u};
-    if (s >= 0x1p-100f) {
-      const float r = __frcp_rn(s);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float t = __fmul_rn(w[e], r);
-        t = __fsub_rn(__fadd_rn(t, 1536.0f), 1536.0f);
-        // |t| <= 7 (1 + 2^-8): the low four bits of the sum's integer are the code
-        q[e >> 3] |= (__float_as_uint(__fadd_rn(t, 12582920.0f)) & 15u) << (4 * (e & 7));
-      }
-    } else {
+    for (int u = 0; u < kPackAt; ++u) {
+      const int64_t i = i0 + u * kPackThreads;
+      float w[8];
+      values8<kFormat>(raw[u], w);
+      uint32_t m = code_max<kFormat>(raw[u]);          // magnitudes' codes order them, NaN above inf
+      for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const float big = code_value<kFormat>(m);
+      const uint16_t sb = big < INFINITY ? f32_to_bf16_rn(__fmul_rn(big, 1.0f / 7.0f)) : (uint16_t)0x7FC0u;
+      const float s = bf16_to_f32(sb);
+      uint32_t q = 0;
+      if (s >= 0x1p-100f) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float t = s > 0.0f ? rintf(__fdiv_rn(w[e], s)) : 0.0f;   // NaN and zero scales: code 8
-        t = fminf(fmaxf(t, -8.0f), 7.0f);
-        q[e >> 3] |= (uint32_t)((int)t + 8) << (4 * (e & 7));
+        for (int e = 7; e >= 0; --e) {
+          // |t| <= 7 (1 + 2^-8): the sum's bits are those of 1.5 2^23 plus the code
+          const float t = __fadd_rn(__fmul_rn(w[e], r), 1536.0f);
+          q = (q << 4) + __float_as_uint(__fadd_rn(t, 12582920.0f - 1536.0f));
+        }
+        q -= kCodeBits;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float t = s > 0.0f ? rintf(__fdiv_rn(w[e], s)) : 0.0f;   // NaN and zero scales: code 8
+          t = fminf(fmaxf(t, -8.0f), 7.0f);
+          q |= (uint32_t)((int)t + 8) << (4 * e);
+        }
       }
-    }
-    if (i < n16) {
-      codes[i] = make_uint2(q[0], q[1]);
-      if ((threadIdx.x & (lanes - 1)) == 0) scales[i / lanes] = sb;
+      if (i < n8) {
+        __stcs(codes + i, q);
+        if ((threadIdx.x & (lanes - 1)) == 0) scales[i / lanes] = sb;
+      }
     }
   }
 }
@@ -131,21 +157,32 @@ __device__ __forceinline__ uint4 q4_values8(uint32_t c, __nv_bfloat162 s2) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-__global__ void __launch_bounds__(kPackThreads) q4_unpack_kernel(const uint2* __restrict__ codes,
-                                                                 const uint16_t* __restrict__ scales, int64_t n16,
-                                                                 int lanes, uint4* __restrict__ W) {
-  const int64_t stride = (int64_t)gridDim.x * kPackThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < n16; i += stride) {
-    const uint2 c = __ldcs(codes + i);
-    const __nv_bfloat16 s = __ushort_as_bfloat16(scales[i / lanes]);
-    const __nv_bfloat162 s2 = __halves2bfloat162(s, s);
-    __stcs(W + 2 * i, q4_values8(c.x, s2));
-    __stcs(W + 2 * i + 1, q4_values8(c.y, s2));
+__global__ void __launch_bounds__(kPackThreads) q4_unpack_kernel(const uint32_t* __restrict__ codes,
+                                                                 const uint16_t* __restrict__ scales, int64_t n8,
+                                                                 int shift, uint4* __restrict__ W) {
+  const int64_t stride = (int64_t)gridDim.x * kPackThreads * kPackAt;
+  for (int64_t i0 = (int64_t)blockIdx.x * kPackThreads * kPackAt + threadIdx.x; i0 < n8; i0 += stride) {
+    uint32_t c[kPackAt];
+    uint16_t s[kPackAt];
+#pragma unroll
+    for (int u = 0; u < kPackAt; ++u) {
+      const int64_t i = i0 + u * kPackThreads;
+      if (i < n8) {
+        c[u] = __ldcs(codes + i);
+        s[u] = __ldg(scales + (i >> shift));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kPackAt; ++u) {
+      const int64_t i = i0 + u * kPackThreads;
+      const __nv_bfloat16 one = __ushort_as_bfloat16(s[u]);
+      if (i < n8) __stcs(W + i, q4_values8(c[u], __halves2bfloat162(one, one)));
+    }
   }
 }
 
-int flat_grid(int64_t threads) {
-  const int64_t want = (threads + kPackThreads - 1) / kPackThreads, most = (int64_t)current_sms() * 16;
+int flat_grid(int64_t vectors) {
+  const int64_t per = kPackThreads * kPackAt, want = (vectors + per - 1) / per, most = (int64_t)current_sms() * 32;
   return (int)(want < most ? want : most);
 }
 
@@ -550,20 +587,26 @@ cudaError_t run_q4_group(const uint8_t* codes, const Q4Args& A, cudaStream_t s) 
 
 cudaError_t launch_q4_pack(const void* W, int64_t L, int32_t d, int w_format, int32_t group, uint8_t* codes,
                            uint16_t* scales, cudaStream_t s) {
-  const int64_t n16 = L * d / 16;
-  const int grid = flat_grid(n16), lanes = group / 16;
-  uint2* c = reinterpret_cast<uint2*>(codes);
-  if (w_format == ELMO_BF16) q4_pack_kernel<ELMO_BF16><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
-  else if (w_format == ELMO_FP8_E5M2) q4_pack_kernel<ELMO_FP8_E5M2><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
-  else q4_pack_kernel<ELMO_FP8_E4M3><<<grid, kPackThreads, 0, s>>>(W, n16, lanes, c, scales);
+  const int64_t n8 = L * d / 8;
+  const int grid = flat_grid(n8), lanes = group / 8;
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  if (w_format == ELMO_BF16)
+    q4_pack_kernel<ELMO_BF16><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_BF16>*>(W), n8, lanes, c, scales);
+  else if (w_format == ELMO_FP8_E5M2)
+    q4_pack_kernel<ELMO_FP8_E5M2><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_FP8_E5M2>*>(W), n8, lanes, c,
+                                                               scales);
+  else
+    q4_pack_kernel<ELMO_FP8_E4M3><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_FP8_E4M3>*>(W), n8, lanes, c,
+                                                               scales);
   return cudaGetLastError();
 }
 
 cudaError_t launch_q4_unpack(const uint8_t* codes, const uint16_t* scales, int64_t L, int32_t d, int32_t group,
                              uint16_t* W, cudaStream_t s) {
-  const int64_t n16 = L * d / 16;
-  q4_unpack_kernel<<<flat_grid(n16), kPackThreads, 0, s>>>(reinterpret_cast<const uint2*>(codes), scales, n16,
-                                                           group / 16, reinterpret_cast<uint4*>(W));
+  const int64_t n8 = L * d / 8;
+  q4_unpack_kernel<<<flat_grid(n8), kPackThreads, 0, s>>>(reinterpret_cast<const uint32_t*>(codes), scales, n8,
+                                                          group == 32 ? 2 : group == 64 ? 3 : 4,
+                                                          reinterpret_cast<uint4*>(W));
   return cudaGetLastError();
 }
 
