@@ -89,27 +89,31 @@ template <int kFormat> __device__ __forceinline__ float code_value(uint32_t m) {
 // sum over e of 16^e times the bits of 1.5 2^23 (0x4B400000), mod 2^32
 constexpr uint32_t kCodeBits = 0x4B400000u * 0x11111111u;
 
-template <int kFormat>
-__global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const Raw8<kFormat>* __restrict__ W, int64_t n8, int lanes,
+// kLanes threads share a group.
+template <int kFormat, int kLanes>
+__global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const Raw8<kFormat>* __restrict__ W, int64_t n8,
                                                                uint32_t* __restrict__ codes,
                                                                uint16_t* __restrict__ scales) {
   // every thread of a warp stays for the shuffles; groups never straddle warps
   const int64_t stride = (int64_t)gridDim.x * kPackThreads * kPackAt;
   for (int64_t i0 = (int64_t)blockIdx.x * kPackThreads * kPackAt + threadIdx.x; i0 - threadIdx.x < n8; i0 += stride) {
+    const int left = (int)min(n8 - i0, (int64_t)kPackThreads * kPackAt);   // vectors from this thread's first on
+    const Raw8<kFormat>* from = W + i0;
+    uint32_t* to = codes + i0;
+    uint16_t* sc = scales + (uint64_t)i0 / kLanes;
     Raw8<kFormat> raw[kPackAt];
 #pragma unroll
     for (int u = 0; u < kPackAt; ++u) {
-      const int64_t i = i0 + u * kPackThreads;
-      if (i < n8) raw[u].v = __ldcs(&W[i].v);
+      if (u * kPackThreads < left) raw[u].v = __ldcs(&from[u * kPackThreads].v);
       else raw[u] = Raw8<kFormat>{};
     }
 #pragma unroll
     for (int u = 0; u < kPackAt; ++u) {
-      const int64_t i = i0 + u * kPackThreads;
       float w[8];
       values8<kFormat>(raw[u], w);
       uint32_t m = code_max<kFormat>(raw[u]);          // magnitudes' codes order them, NaN above inf
-      for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+#pragma unroll
+      for (int o = kLanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       const float big = code_value<kFormat>(m);
       const uint16_t sb = big < INFINITY ? f32_to_bf16_rn(__fmul_rn(big, 1.0f / 7.0f)) : (uint16_t)0x7FC0u;
       const float s = bf16_to_f32(sb);
@@ -132,9 +136,9 @@ __global__ void __launch_bounds__(kPackThreads) q4_pack_kernel(const Raw8<kForma
           q |= (uint32_t)((int)t + 8) << (4 * e);
         }
       }
-      if (i < n8) {
-        __stcs(codes + i, q);
-        if ((threadIdx.x & (lanes - 1)) == 0) scales[i / lanes] = sb;
+      if (u * kPackThreads < left) {
+        __stcs(to + u * kPackThreads, q);
+        if (threadIdx.x % kLanes == 0) sc[u * (kPackThreads / kLanes)] = sb;
       }
     }
   }
@@ -184,6 +188,16 @@ __global__ void __launch_bounds__(kPackThreads) q4_unpack_kernel(const uint32_t*
 int flat_grid(int64_t vectors) {
   const int64_t per = kPackThreads * kPackAt, want = (vectors + per - 1) / per, most = (int64_t)current_sms() * 32;
   return (int)(want < most ? want : most);
+}
+
+template <int kFormat>
+cudaError_t run_pack(const void* W, int64_t n8, int32_t group, uint32_t* codes, uint16_t* scales, cudaStream_t s) {
+  const Raw8<kFormat>* w = static_cast<const Raw8<kFormat>*>(W);
+  const int grid = flat_grid(n8);
+  if (group == 32) q4_pack_kernel<kFormat, 4><<<grid, kPackThreads, 0, s>>>(w, n8, codes, scales);
+  else if (group == 64) q4_pack_kernel<kFormat, 8><<<grid, kPackThreads, 0, s>>>(w, n8, codes, scales);
+  else q4_pack_kernel<kFormat, 16><<<grid, kPackThreads, 0, s>>>(w, n8, codes, scales);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- scores
@@ -588,17 +602,10 @@ cudaError_t run_q4_group(const uint8_t* codes, const Q4Args& A, cudaStream_t s) 
 cudaError_t launch_q4_pack(const void* W, int64_t L, int32_t d, int w_format, int32_t group, uint8_t* codes,
                            uint16_t* scales, cudaStream_t s) {
   const int64_t n8 = L * d / 8;
-  const int grid = flat_grid(n8), lanes = group / 8;
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  if (w_format == ELMO_BF16)
-    q4_pack_kernel<ELMO_BF16><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_BF16>*>(W), n8, lanes, c, scales);
-  else if (w_format == ELMO_FP8_E5M2)
-    q4_pack_kernel<ELMO_FP8_E5M2><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_FP8_E5M2>*>(W), n8, lanes, c,
-                                                               scales);
-  else
-    q4_pack_kernel<ELMO_FP8_E4M3><<<grid, kPackThreads, 0, s>>>(static_cast<const Raw8<ELMO_FP8_E4M3>*>(W), n8, lanes, c,
-                                                               scales);
-  return cudaGetLastError();
+  if (w_format == ELMO_BF16) return run_pack<ELMO_BF16>(W, n8, group, c, scales, s);
+  if (w_format == ELMO_FP8_E5M2) return run_pack<ELMO_FP8_E5M2>(W, n8, group, c, scales, s);
+  return run_pack<ELMO_FP8_E4M3>(W, n8, group, c, scales, s);
 }
 
 cudaError_t launch_q4_unpack(const uint8_t* codes, const uint16_t* scales, int64_t L, int32_t d, int32_t group,
