@@ -540,6 +540,7 @@ __device__ __forceinline__ void near_scores(const uint16_t* X, const void* W, co
                                             float (&acc)[kM]) {
 #pragma unroll
   for (int m = 0; m < kM; ++m) acc[m] = 0.0f;
+#pragma unroll 3
   for (int c = lane; c < d / 8; c += 32) {
     Raw8<kFormat> r[kM];
 #pragma unroll
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
       if (ok) each([&](int, int, float v) { best = fmaxf(best, v); });
       const float low = lower_bound_kth<kJoinThreads>(&S, best, A.k);
       const float from = __fsub_rd(low, __fdiv_ru(two, inv));
-      if (ok)
+      if (ok && best >= from)                          // a thread that has seen none has none to list
         each([&](int i, int e, float v) {
           if (v >= from && v > -INFINITY) {
             const int at = atomicAdd(&nblocks, 1);
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
 // 64 best among 3M 8-bit labels: 0.9 GB), by latency else: every load of a
 // step starts before the first is used, and the query comes from L1.
 template <int kFormat>
-__global__ void __launch_bounds__(kNearThreads) label_near_kernel(const Args A, int tile) {
+__global__ void __launch_bounds__(kNearThreads, 2) label_near_kernel(const Args A, int tile) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();

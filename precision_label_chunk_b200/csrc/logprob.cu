@@ -529,11 +529,13 @@ __global__ void __launch_bounds__(kJoinThreads) score_row_kernel(const Args A) {
 // With g_i, g_lse and g_H the gradients of the row's log p of label c_i, lse
 // and entropy H:
 //     dz_l = sum_{i: c_i = l} g_i + p_l (g_lse - sum_i g_i - g_H (log p_l + H)).
-// One pass that reads z and writes dz (HBM-bound); the CTA of a segment first
-// gathers the segment's given labels into a row of addends, so that a label
-// given twice gets the sum in the order of the list, each dz is rounded once,
-// and dz may take z's place.
-constexpr int kSeg = 4096;
+// One pass that reads z and writes dz (HBM-bound), a warp a segment: its scores
+// are on their way while it goes through the row's list, and no warp waits for
+// another (a CTA a segment of 4096, with barriers around the list, took 100 us
+// for 256 rows of 500K bf16 scores).  The segment's given labels go into a row
+// of addends first, so that a label given twice gets the sum in the order of
+// the list, each dz is rounded once, and dz may take z's place.
+constexpr int kSeg = 1024;
 
 struct BwdArgs {
   const void* Z;
@@ -549,71 +551,64 @@ template <> __device__ __forceinline__ void put_grad<float>(float* p, float v) {
 template <> __device__ __forceinline__ void put_grad<uint16_t>(uint16_t* p, float v) { *p = f32_to_bf16_rn(v); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) score_backward_kernel(const BwdArgs A) {
-  constexpr int kE = Vec<T>::kE;
-  __shared__ float addend[kSeg];
-  __shared__ int32_t ids[kThreads];
-  __shared__ float gs[kThreads];
-  __shared__ double red[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(kThreads, 4) score_backward_kernel(const BwdArgs A) {
+  constexpr int kE = Vec<T>::kE, kV = Vec<T>::kV;
+  __shared__ float addends[kWarps][kSeg];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* addend = addends[warp];
   const int64_t b = blockIdx.y;
   const T* z = static_cast<const T*>(A.Z) + b * A.ldz;
   T* dz = static_cast<T*>(A.dZ) + b * A.lddz;
   const int shift = shift_of(z);
-  const int64_t first = (int64_t)blockIdx.x * kSeg - shift;       // the segment's labels: [first, first + kSeg)
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) * kSeg - shift;   // the labels [first, first + kSeg)
+  if (first >= A.L) return;
+  const bool whole = first >= 0 && first + kSeg <= A.L && shift_of(dz) == shift;
+  uint4 q[kV];
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(z + first) + 32 * i + lane);
+  }
   const float lse = A.lse[b];
   const bool dead = isinf(lse);                                   // no label, or no softmax: no gradient
 
-  // the scores before anything that waits for the row's lists
-  constexpr int kVecs = kSeg / (kThreads * kE);
-  const bool whole = first >= 0 && first + kSeg <= A.L && shift_of(dz) == shift;
-  uint4 q[kVecs];
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(z + first) + i * kThreads + tid);
-  }
-
   double sum = 0.0;
   bool any = false;
-  const int e0 = max(A.rowptr[b], 0), e1 = min(A.rowptr[b + 1], A.nnz);
+  const int e0 = min(max(A.rowptr[b], 0), A.nnz), e1 = min(A.rowptr[b + 1], A.nnz);
   if (A.g_logp && !dead) {
-    for (int e = e0 + tid; e < e1; e += kThreads) {
+    for (int e = e0 + lane; e < e1; e += 32) {
       const int32_t l = A.cols[e];
       if (l < 0 || l >= A.L) continue;
       sum += A.g_logp[e];
       any |= l >= first && l < first + kSeg;
     }
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) red[warp] = sum;
-    any = __syncthreads_or(any);
-    sum = 0.0;
-    for (int w = 0; w < kWarps; ++w) sum += red[w];
+    any = __any_sync(0xFFFFFFFFu, any);
   }
   if (any) {
-    for (int i = tid; i < kSeg; i += kThreads) addend[i] = 0.0f;
-    for (int base = e0; base < e1; base += kThreads) {
-      const int e = base + tid;
+    for (int i = lane; i < kSeg; i += 32) addend[i] = 0.0f;
+    for (int base = e0; base < e1; base += 32) {
+      const int e = base + lane;
       int32_t l = -1;
+      float g = 0.0f;
       if (e < e1) {
         l = A.cols[e];
         if (l < 0 || l >= A.L || l < first || l >= first + kSeg) l = -1;
+        else g = A.g_logp[e];
       }
-      if (!__syncthreads_or(l >= 0)) continue;                    // also: addend is clear, the last round's reads are done
-      ids[tid] = l;
-      if (l >= 0) gs[tid] = A.g_logp[e];
-      __syncthreads();
-      if (l >= 0) {
-        bool mine = true;
-        for (int j = 0; j < tid && mine; ++j) mine = ids[j] != l;
-        if (mine) {
-          float g = addend[l - first];
-          for (int j = tid; j < kThreads && base + j < e1; ++j)
-            if (ids[j] == l) g += gs[j];
-          addend[l - first] = g;
-        }
+      if (!__any_sync(0xFFFFFFFFu, l >= 0)) continue;
+      // the first lane that has a label adds those of all that have it, in order
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, l);
+      const bool leads = l >= 0 && (same & ((1u << lane) - 1u)) == 0;
+      __syncwarp();
+      float acc = leads ? addend[l - first] : 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const float gj = __shfl_sync(0xFFFFFFFFu, g, j);
+        if ((same >> j) & 1u) acc += gj;
       }
+      if (leads) addend[l - first] = acc;
     }
-    __syncthreads();
+    __syncwarp();
   }
 
   const float gH = A.g_entropy ? A.g_entropy[b] : 0.0f;
@@ -632,8 +627,7 @@ __global__ void __launch_bounds__(kThreads) score_backward_kernel(const BwdArgs 
   };
   if (whole && !dead) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int i0 = (i * kThreads + tid) * kE;
+    for (int i = 0; i < kV; ++i) {
       const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
       float r[kE];
 #pragma unroll
@@ -643,15 +637,15 @@ __global__ void __launch_bounds__(kThreads) score_backward_kernel(const BwdArgs 
       }
       if (any) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) r[e] += addend[i0 + e];
+        for (int e = 0; e < kE; ++e) r[e] += addend[(32 * i + lane) * kE + e];
       }
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = sizeof(T) == 4 ? __float_as_uint(r[e]) : pack_bf16x2(r[(2 * e + 1) % kE], r[(2 * e) % kE]);
-      __stcs(reinterpret_cast<uint4*>(dz + first) + i * kThreads + tid, make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(reinterpret_cast<uint4*>(dz + first) + 32 * i + lane, make_uint4(o[0], o[1], o[2], o[3]));
     }
   } else {
-    for (int i = tid; i < kSeg; i += kThreads) {
+    for (int i = lane; i < kSeg; i += 32) {
       const int64_t l = first + i;
       if (l < 0 || l >= A.L) continue;
       float r = dead ? 0.0f : grad(score_at(z, l));
@@ -710,7 +704,7 @@ cudaError_t launch_score_backward(const void* Z, bool bf16, int64_t ldz, int32_t
                                   const float* g_logp, const float* g_lse, const float* g_entropy, void* dZ,
                                   int64_t lddz, cudaStream_t s) {
   const BwdArgs A{Z, dZ, ldz, lddz, L, nnz, rowptr, cols, lse, entropy, g_logp, g_lse, g_entropy};
-  const dim3 grid((unsigned)((L + 7 + kSeg - 1) / kSeg), (unsigned)B);
+  const dim3 grid((unsigned)((L + 7 + kSeg * kWarps - 1) / (kSeg * kWarps)), (unsigned)B);
   if (bf16) score_backward_kernel<uint16_t><<<grid, kThreads, 0, s>>>(A);
   else score_backward_kernel<float><<<grid, kThreads, 0, s>>>(A);
   return cudaGetLastError();
