@@ -551,7 +551,7 @@ template <> __device__ __forceinline__ void put_grad<float>(float* p, float v) {
 template <> __device__ __forceinline__ void put_grad<uint16_t>(uint16_t* p, float v) { *p = f32_to_bf16_rn(v); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) score_backward_kernel(const BwdArgs A) {
+__global__ void __launch_bounds__(kThreads, 5) score_backward_kernel(const BwdArgs A) {
   constexpr int kE = Vec<T>::kE, kV = Vec<T>::kV;
   __shared__ float addends[kWarps][kSeg];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
