@@ -548,7 +548,7 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
 
 /*
  * elmo_label_logprobs -- the statistics of elmo_score_logprobs straight from
- * the head: no score is stored.
+ * the head, without a matrix of scores.
  *
  * Passage: the label axis is processed in chunks so that no full logit matrix
  * exists (atlas summary, "Approach").  The scores are z = x . w_l over all L

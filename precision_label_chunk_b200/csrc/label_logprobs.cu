@@ -28,7 +28,10 @@
 //      2 delta, delta the error bound of those scores: the blocks with a
 //      maximum of at least low - 2 delta hold all of the k best.  Their labels
 //      are scored again in fp32, which narrows them down the same way, and
-//      what is left is ranked by exact scores.
+//      what is left is ranked by exact scores.  Heads of few labels keep all
+//      their tensor-core scores in place of the maxima: with fewer blocks than
+//      a few times k, most labels would be scored again (1571 labels, 180
+//      queries, 5 best: 86 us).
 //   4. queries with too many labels within 2 delta (ties), or a head that is
 //      not finite, rank all labels by exact scores on the CUDA cores.
 //
@@ -58,6 +61,8 @@ constexpr long long kWait = 4000000000LL; // ~2 s
 constexpr float kNoLabel = -3.0e38f;      // a score that e^ takes to 0 and whose product with it is 0
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr size_t kMaxima = size_t(256) << 20;   // bytes of block maxima, about
+constexpr int64_t kKeepLabels = 16384;    // heads of up to so many labels keep every score instead,
+constexpr size_t kKeepBytes = size_t(64) << 20;   // if they take no more than this
 constexpr int kJoinThreads = 512;
 constexpr int kGroups = 256;              // groups whose best give the lower bound on the k-th best
 constexpr int kMaxBlocks = 256;           // blocks that are scored again for a query,
@@ -90,12 +95,13 @@ struct Args {
   int32_t d, B, G, k, nnz, fmt;
   int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
   int32_t nblk, nblkp, pairs;             // blocks of a parity, with padding; tiles of a block
+  int32_t parities;                       // 2; 0 where every label's score is kept: nblkp is their pitch
   float gamma;
   float *xinv, *n1, *r1;
   int32_t *rflag, *fail;
   int32_t* done;                          // [B] segments of a failed query that are ranked
   Counts* counts;
-  float* bmax;                            // [B][2][nblkp] maxima of the accumulators over blocks
+  float* bmax;                            // [B][2][nblkp] maxima of the accumulators over blocks, or [B][nblkp] of all
   int2* items;                            // (query, block) to be scored again, at most kMaxBlocks a query
   int32_t *listed, *nnear;                  // [B] whether the query's blocks are listed; labels found near
   float* near_v;                          // [B][kMaxNear] their fp32 scores
@@ -229,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int P = (A.B + 127) / 128;
   const int p = blockIdx.x % P, g = blockIdx.x / P;
   const int64_t T = (A.L + kN - 1) / kN;
-  const int64_t blk0 = (int64_t)A.nblk * g / A.G, blk1 = (int64_t)A.nblk * (g + 1) / A.G;
+  const int64_t nrange = (T + 2 * A.pairs - 1) / (2 * A.pairs);
+  const int64_t blk0 = nrange * g / A.G, blk1 = nrange * (g + 1) / A.G;
   const int64_t t0 = 2 * blk0 * A.pairs, t1 = min(T, 2 * blk1 * A.pairs);
   const int nkb = (A.d + kKE - 1) / kKE;
   const int nst = (nkb + A.kbs - 1) / A.kbs;           // stages of a group of q tiles (1 where q > 1)
@@ -254,22 +261,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp != 0 || kXs) pdl_wait();
 
   if (!kXs) {
-    if (warp >= 2 && warp < 6) {                       // query r of the panel into lane r
+    if (warp >= 2 && warp < 10) {                      // query r of the panel into lane r, 32 columns at a time
       const int quad = warp & 3, row = p * 128 + quad * 32 + lane;
       const size_t rowbytes = (size_t)A.d * (kFp8 ? 1 : 2);
-      for (int op = 0; op < kOps; ++op) {
+      // two pieces' loads in flight: one piece at a time kept the first MMA waiting for 10 us
+#pragma unroll 2
+      for (uint32_t piece = (warp - 2) >> 2; piece < (uint32_t)kOps * nkb; piece += 2) {
+        const uint32_t op = piece / nkb, c0 = piece % nkb * 32;
         const uint8_t* src = (kFp8 ? (op ? A.xb : A.xa) : reinterpret_cast<const uint8_t*>(A.X)) + (size_t)row * rowbytes;
-        for (uint32_t c0 = 0; c0 < opcols; c0 += 32) {
-          uint32_t v[32];
+        uint32_t v[32];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const size_t off = (size_t)(c0 + 4 * u) * 4;
-            uint4 w4 = make_uint4(0u, 0u, 0u, 0u);
-            if (row < A.B && off < rowbytes) w4 = *reinterpret_cast<const uint4*>(src + off);
-            v[4 * u] = w4.x; v[4 * u + 1] = w4.y; v[4 * u + 2] = w4.z; v[4 * u + 3] = w4.w;
-          }
-          tmem_st32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)op * opcols + c0, v);
+        for (int u = 0; u < 8; ++u) {
+          const size_t off = (size_t)(c0 + 4 * u) * 4;
+          uint4 w4 = make_uint4(0u, 0u, 0u, 0u);
+          if (row < A.B && off < rowbytes) w4 = *reinterpret_cast<const uint4*>(src + off);
+          v[4 * u] = w4.x; v[4 * u + 1] = w4.y; v[4 * u + 2] = w4.z; v[4 * u + 3] = w4.w;
         }
+        tmem_st32(tmem + ((uint32_t)(quad * 32) << 16) + op * opcols + c0, v);
       }
       tmem_wait_st();
     }
@@ -368,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = row < A.B;
     const float inv = live ? A.xinv[row] : 1.0f;
     Soft soft(inv);
-    float* bm = A.bmax + ((size_t)row * 2 + par) * A.nblkp;
+    const bool keep = A.k > 0 && A.parities == 0;
+    float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * 2 + par) * A.nblkp;
     float win[8];                                      // maxima of the aligned eight blocks under way
     uint32_t nt = 0;
     bool ok = true;
@@ -409,10 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mx = max32(v);
             best = fmaxf(best, mx);
             soft.add32<false>(v, mx);
+            if (keep) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4)
+                if (l0 + 32 * h + c < A.nblkp)
+                  *reinterpret_cast<float4*>(bm + l0 + 32 * h + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+            }
           }
         }
       }
-      if (A.k > 0 && live) {
+      if (A.k > 0 && !keep && live) {
         const int j = (int)blk & 7;
 #pragma unroll
         for (int e = 0; e < 8; ++e) win[e] = e == j ? best : win[e];
@@ -704,54 +719,81 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     } else {
       const float two = two_delta(A, b), inv = A.xinv[b];
       bool ok = two < INFINITY;                        // not so for weights that are not finite
-      const float4* bm = reinterpret_cast<const float4*>(A.bmax + (size_t)b * 2 * A.nblkp);
-      const int n4 = A.nblkp / 2;                      // vectors of both parities
-      // entry e of vector i is block (4 i + e) mod nblkp of parity 4 i >= nblkp
-      auto count_of = [&](int i) { return min(4, A.nblk - (4 * i < A.nblkp ? 4 * i : 4 * i - A.nblkp)); };
+      // n maxima: entry i < nblkp is block i of parity 0, then those of parity 1;
+      // or all the labels' scores
+      const bool keep = A.parities == 0;
+      const float* bm = A.bmax + (size_t)b * (keep ? 1 : 2) * A.nblkp;
+      const int n = keep ? (int)A.L : A.nblkp + A.nblk;
+      auto none = [&](int i) { return !keep && i >= A.nblk && i < A.nblkp; };   // padding
       auto each = [&](auto f) {
-        for (int i0 = tid; i0 < n4; i0 += 8 * kJoinThreads) {
-          float4 v[8];
+        if (n <= kGroups) {                            // one to a group
+          if (tid % (kJoinThreads / kGroups) == 0 && tid / (kJoinThreads / kGroups) < n) {
+            const int i = tid / (kJoinThreads / kGroups);
+            if (!none(i)) f(i, __ldcg(bm + i));
+          }
+        } else if (n <= 4 * kJoinThreads) {
+          float v[4];
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (i0 + u * kJoinThreads < n4) v[u] = __ldcg(bm + i0 + u * kJoinThreads);
+          for (int u = 0; u < 4; ++u)
+            if (tid + u * kJoinThreads < n) v[u] = __ldcg(bm + tid + u * kJoinThreads);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * kJoinThreads;
-            if (i >= n4) break;
-            const int c = count_of(i);
-            if (c > 0) f(i, 0, v[u].x);
-            if (c > 1) f(i, 1, v[u].y);
-            if (c > 2) f(i, 2, v[u].z);
-            if (c > 3) f(i, 3, v[u].w);
+          for (int u = 0; u < 4; ++u) {
+            const int i = tid + u * kJoinThreads;
+            if (i < n && !none(i)) f(i, v[u]);
+          }
+        } else {
+          const int n4 = (n + 3) / 4;
+          for (int i0 = tid; i0 < n4; i0 += 8 * kJoinThreads) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (i0 + u * kJoinThreads < n4) v[u] = __ldcg(reinterpret_cast<const float4*>(bm) + i0 + u * kJoinThreads);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = 4 * (i0 + u * kJoinThreads);
+              const float w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (i + e < n && !none(i + e)) f(i + e, w[e]);
+            }
           }
         }
       };
       float best = -INFINITY;
-      if (ok) each([&](int, int, float v) { best = fmaxf(best, v); });
+      if (ok) each([&](int, float v) { best = fmaxf(best, v); });
       const float low = lower_bound_kth<kJoinThreads>(&S, best, A.k);
       const float from = __fsub_rd(low, __fdiv_ru(two, inv));
       if (ok && best >= from)                          // a thread that has seen none has none to list
-        each([&](int i, int e, float v) {
+        each([&](int i, float v) {
           if (v >= from && v > -INFINITY) {
             const int at = atomicAdd(&nblocks, 1);
-            if (at < kMaxBlocks) blocks[at] = 4 * i + e;
+            if (keep) {
+              if (at < kMaxNear) {
+                A.near_v[(size_t)b * kMaxNear + at] = __fmul_rn(v, inv);
+                A.near_l[(size_t)b * kMaxNear + at] = i;
+              }
+            } else if (at < kMaxBlocks) {
+              blocks[at] = i;
+            }
           }
         });
       __syncthreads();
-      const int n = nblocks;
-      ok = ok && n > 0 && n <= kMaxBlocks;
+      const int found = nblocks;
+      ok = ok && found > 0 && found <= (keep ? kMaxNear : kMaxBlocks);
       if (tid == 0) {
         A.listed[b] = ok;
-        if (ok) {
-          at0 = atomicAdd(&A.counts->nitems, n);
-          A.from[b] = __fsub_rd(__fmul_rd(low, inv), two);
-        } else {
+        if (!ok) {
           A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
+        } else if (keep) {
+          A.nnear[b] = found;
+        } else {
+          at0 = atomicAdd(&A.counts->nitems, found);
+          A.from[b] = __fsub_rd(__fmul_rd(low, inv), two);
         }
       }
       __syncthreads();
-      if (ok)
-        for (int i = tid; i < n; i += kJoinThreads) A.items[at0 + i] = make_int2(b, blocks[i]);
+      if (ok && !keep)
+        for (int i = tid; i < found; i += kJoinThreads) A.items[at0 + i] = make_int2(b, blocks[i]);
     }
   }
 
@@ -989,7 +1031,7 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
 
 // ---------------------------------------------------------------- host
 struct Layout {
-  int G, nblk, nblkp, pairs;
+  int G, nblk, nblkp, pairs, parities;
   size_t xa, xb, xinv, n1, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
       rowstat, total;
 };
@@ -1002,12 +1044,14 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   const int P = (B + 127) / 128;
   const int64_t N = tile_labels(h), T = (h->L + N - 1) / N;
   o.pairs = 1;
-  if (k > 0)
+  o.parities = k > 0 && h->L <= kKeepLabels && (size_t)B * h->L * 4 <= kKeepBytes ? 0 : 2;
+  if (k > 0 && o.parities)
     while ((size_t)B * (T / o.pairs) * 4 > kMaxima) o.pairs *= 2;
   o.nblk = (int)((T + 2 * o.pairs - 1) / (2 * o.pairs));
-  o.nblkp = (o.nblk + 7) / 8 * 8;
   int64_t G = h->num_sms / P;
   if (G > o.nblk) G = o.nblk;
+  if (o.parities == 0) o.nblk = (int)h->L;
+  o.nblkp = (o.nblk + 7) / 8 * 8;
   if (G < 1) G = 1;
   o.G = (int)G;
   size_t off = 0;
@@ -1028,7 +1072,7 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   o.near_v = take(4 * lists * kMaxNear);
   o.near_l = take(4 * lists * kMaxNear);
   o.from = take(4 * lists);
-  o.bmax = take(k > 0 ? 8 * (size_t)B * o.nblkp : 0);
+  o.bmax = take(k > 0 ? (o.parities ? 8 : 4) * (size_t)B * o.nblkp : 0);
   o.part = take(sizeof(Stat) * (size_t)B * 2 * o.G);
   o.sk = take(8 * (size_t)B * kSegs * k);
   o.si = take(4 * (size_t)B * kSegs * k);
@@ -1076,8 +1120,10 @@ cudaError_t run_join(elmo_head* h, const Args& A, cudaStream_t s) {
   const size_t xbytes = sizeof(float) * (size_t)h->d;
   cudaError_t e = launch_after(label_join_kernel<kFormat>, dim3(A.B), kJoinThreads, xbytes, s, A);
   if (e != cudaSuccess || A.k == 0) return e;
-  e = launch_after(label_near_kernel<kFormat>, dim3(h->num_sms * 4), kNearThreads, 0, s, A, tile_labels(h));
-  if (e != cudaSuccess) return e;
+  if (A.parities != 0) {
+    e = launch_after(label_near_kernel<kFormat>, dim3(h->num_sms * 4), kNearThreads, 0, s, A, tile_labels(h));
+    if (e != cudaSuccess) return e;
+  }
   e = launch_after(label_rank_kernel<kFormat>, dim3(A.B), kNearThreads, xbytes, s, A);
   if (e != cudaSuccess) return e;
   return launch_after(label_exact_kernel<kFormat>, dim3(h->num_sms * 2), kExactThreads, xbytes, s, A);
@@ -1103,7 +1149,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.label_base = h->label_base;
   A.labels_total = h->labels_total;
   A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.nnz = nnz;
-  A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs;
+  A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.parities = o.parities;
   A.fmt = w_format(h);
   const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
   A.gamma = (float)nsteps * 0x1p-22f;
@@ -1142,7 +1188,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
     else e = wide ? run_pass<1, 0, 1>(h, A, s) : run_pass<1, 0, 0>(h, A, s);
     if (e != cudaSuccess) return e;
   }
-  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k > 0 ? 4 : 1);
+  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.parities ? 4 : 3);
   if (A.fmt == ELMO_BF16) return run_join<ELMO_BF16>(h, A, s);
   if (A.fmt == ELMO_FP8_E5M2) return run_join<ELMO_FP8_E5M2>(h, A, s);
   return run_join<ELMO_FP8_E4M3>(h, A, s);
