@@ -54,7 +54,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;             // warp 0 TMA, 1 MMA and TMEM, 2-9 epilogue, 10-11 max|W|
+constexpr int kStreams = 4;               // groups of four epilogue warps: even or odd tiles, left or right half
+constexpr int kEpi = 2 + 4 * kStreams;    // warp 0 TMA, 1 MMA and TMEM, 2 .. kEpi - 1 epilogue, then two for max|W|
+constexpr int kThreads = 32 * (kEpi + 2);
 constexpr int kMaxStages = 16;
 constexpr uint32_t kAccCol = 384;         // first accumulator column where X lies in TMEM
 constexpr long long kWait = 4000000000LL; // ~2 s
@@ -94,20 +96,20 @@ struct Args {
   int64_t L, label_base, labels_total;
   int32_t d, B, G, k, nnz, fmt;
   int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
-  int32_t nblk, nblkp, pairs;             // blocks of a parity, with padding; tiles of a block
-  int32_t parities;                       // 2; 0 where every label's score is kept: nblkp is their pitch
+  int32_t nblk, nblkp, pairs;             // blocks of a stream, with padding; half tiles of a block
+  int32_t streams;                        // kStreams; 0 where every label's score is kept: nblkp is their pitch
   float gamma;
   float *xinv, *n1, *r1;
   int32_t *rflag, *fail;
   int32_t* done;                          // [B] segments of a failed query that are ranked
   Counts* counts;
-  float* bmax;                            // [B][2][nblkp] maxima of the accumulators over blocks, or [B][nblkp] of all
+  float* bmax;                            // [B][kStreams][nblkp] maxima of the accumulators over blocks, or [B][nblkp] of all
   int2* items;                            // (query, block) to be scored again, at most kMaxBlocks a query
   int32_t *listed, *nnear;                  // [B] whether the query's blocks are listed; labels found near
   float* near_v;                          // [B][kMaxNear] their fp32 scores
   int32_t* near_l;
   float* from;                            // [B] the fp32 score from which a label is near
-  Stat* part;                             // [B][2 G]
+  Stat* part;                             // [B][kStreams G]
   uint64_t* seg_key;                      // [B][kSegs][k]
   int32_t* seg_i;
   const int32_t *rowptr, *cols;
@@ -117,9 +119,10 @@ struct Args {
   int32_t* status;
 };
 
-// Tiles of even and odd number go to two groups of epilogue warps.  Block i
-// of a parity is the `pairs` tiles 2 (i pairs + r) + parity, and a range is a
-// run of blocks of both parities.
+// A tile's accumulators go to two groups of four epilogue warps, a half each;
+// tiles of even and odd number have groups of their own.  Block i of stream
+// 2 (tile & 1) + half is that half of the `pairs` tiles 2 (i pairs + r) +
+// (tile & 1), and a range is a run of blocks of all streams.
 
 // ---------------------------------------------------------------- 1. operands
 constexpr int kPrepThreads = 128;
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < A.stages; ++s) { mbar_init(&S->full[s], 1); mbar_init(&S->empty[s], scan ? 3 : 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 4); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 8); }
     S->abort = 0;
     fence_barrier_init();
   }
@@ -261,12 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp != 0 || kXs) pdl_wait();
 
   if (!kXs) {
-    if (warp >= 2 && warp < 10) {                      // query r of the panel into lane r, 32 columns at a time
+    if (warp >= 2 && warp < kEpi) {                    // query r of the panel into lane r, 32 columns at a time
       const int quad = warp & 3, row = p * 128 + quad * 32 + lane;
       const size_t rowbytes = (size_t)A.d * (kFp8 ? 1 : 2);
       // two pieces' loads in flight: one piece at a time kept the first MMA waiting for 10 us
 #pragma unroll 2
-      for (uint32_t piece = (warp - 2) >> 2; piece < (uint32_t)kOps * nkb; piece += 2) {
+      for (uint32_t piece = (warp - 2) >> 2; piece < (uint32_t)kOps * nkb; piece += kStreams) {
         const uint32_t op = piece / nkb, c0 = piece % nkb * 32;
         const uint8_t* src = (kFp8 ? (op ? A.xb : A.xa) : reinterpret_cast<const uint8_t*>(A.X)) + (size_t)row * rowbytes;
         uint32_t v[32];
@@ -370,15 +373,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 10) {
-    const int par = (warp - 2) >> 2;                   // tiles of this parity (t0 is even)
+  } else if (warp < kEpi) {
+    // The score of a query and label costs some 7 issue slots and one
+    // exponential, and a warp on its own starts an instruction every 6 cycles:
+    // four warps a scheduler bring the epilogue below the other bounds (two
+    // took 93 us for 1M labels x 256 and 105 queries).
+    const int stream = (warp - 2) >> 2, par = stream >> 1, half = stream & 1;   // t0 is even
     const int quad = warp & 3, r = quad * 32 + lane, row = p * 128 + r;
     const bool live = row < A.B;
-    const float inv = live ? A.xinv[row] : 1.0f;
+    const float inv = live ? A.xinv[row] : 1.0f;       // scores are inv times the accumulators
     Soft soft(inv);
-    const bool keep = A.k > 0 && A.parities == 0;
-    float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * 2 + par) * A.nblkp;
+    const bool keep = A.k > 0 && A.streams == 0;
+    float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * kStreams + stream) * A.nblkp;
     float win[8];                                      // maxima of the aligned eight blocks under way
+#pragma unroll
+    for (int e = 0; e < 8; ++e) win[e] = -INFINITY;
     uint32_t nt = 0;
     bool ok = true;
     for (int64_t blk = blk0; blk < blk1 && ok; ++blk) {
@@ -392,38 +401,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int u = 0; u < kN / 64; ++u) {
           __syncwarp();
-          uint32_t raw[2][32];
-          const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (kXs ? 0 : kAccCol) + par * kN + u * 64;
-          tmem_ld32(at, raw[0]);
-          tmem_ld32(at + 32, raw[1]);
+          uint32_t raw[32];
+          tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + (kXs ? 0 : kAccCol) + par * kN + half * (kN / 2) + u * 32, raw);
           tmem_wait_ld();
           if (u == kN / 64 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&S->tempty[par]);
           }
-          if (!live) continue;
-          const int64_t l0 = tile * kN + u * 64;
-          if (l0 + 64 > A.L) {                         // past the end there are no labels
+          const int64_t l0 = tile * kN + half * (kN / 2) + u * 32;
+          if (!live || l0 >= A.L) continue;
+          float v[32];
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (l0 + c >= A.L) raw[c >> 5][c & 31] = __float_as_uint(kNoLabel);
+          for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[c]);
+          if (l0 + 32 > A.L) {                         // past the end there are no labels
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (l0 + c >= A.L) v[c] = kNoLabel;
           }
+          const float mx = max32(v);
+          best = fmaxf(best, mx);
+          soft.add32<false>(v, mx);
+          if (keep) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (l0 + 32 * h >= A.L) break;
-            float v[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[h][c]);
-            const float mx = max32(v);
-            best = fmaxf(best, mx);
-            soft.add32<false>(v, mx);
-            if (keep) {
-#pragma unroll
-              for (int c = 0; c < 32; c += 4)
-                if (l0 + 32 * h + c < A.nblkp)
-                  *reinterpret_cast<float4*>(bm + l0 + 32 * h + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-            }
+            for (int c = 0; c < 32; c += 4)
+              if (l0 + c < A.nblkp) *reinterpret_cast<float4*>(bm + l0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
           }
         }
       }
@@ -431,26 +433,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = (int)blk & 7;
 #pragma unroll
         for (int e = 0; e < 8; ++e) win[e] = e == j ? best : win[e];
+        const bool end = blk + 1 == A.nblk;            // of the row: the padding holds nothing
         if (j == 7 || blk + 1 == blk1) {
           const int64_t first = blk - j;
-          if (j == 7 && first >= blk0) {
+          if (first >= blk0 && (j == 7 || end)) {
             reinterpret_cast<float4*>(bm + first)[0] = make_float4(win[0], win[1], win[2], win[3]);
             reinterpret_cast<float4*>(bm + first)[1] = make_float4(win[4], win[5], win[6], win[7]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (e <= j && first + e >= blk0) bm[first + e] = win[e];
+              if ((e <= j || end) && first + e >= blk0) bm[first + e] = win[e];
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) win[e] = -INFINITY;
         }
       }
     }
-    if (live) A.part[(size_t)row * 2 * A.G + 2 * g + par] = {soft.m * inv, soft.s, soft.t * inv};
+    if (live) A.part[((size_t)row * A.G + g) * kStreams + stream] = {soft.m * inv, soft.s, soft.t * inv};
   } else if (scan) {
     // bf16 magnitudes by 16-bit maxima, two instructions for two weights.  Of
     // 8-bit magnitudes x, x + (0x7F - m) carries into the sign bit exactly
     // where x exceeds the largest so far, m: two and a half for four, and m
     // seldom moves.  Panels of one range take its stages in turn.
-    const int id = (warp - 10) * 32 + lane;
+    const int id = (warp - kEpi) * 32 + lane;
     uint32_t mx = 0, s = 0, ph = 0, turn = 0;
     bool ok = true;
     for (int64_t t = t0; t < t1 && ok && !*abort; t += A.q) {
@@ -656,8 +661,8 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   pdl_trigger();
   const bool bad = A.rflag[b] != 0;
   {
-    // at most two partial sums of a thread: 2 G <= 2 SMs
-    const int n = 2 * A.G;
+    // at most two partial sums of a thread: kStreams G, G at most the SMs
+    const int n = kStreams * A.G;
     const Stat* part = A.part + (size_t)b * n;
     Stat q[2];
     float mf = -INFINITY;
@@ -719,17 +724,15 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     } else {
       const float two = two_delta(A, b), inv = A.xinv[b];
       bool ok = two < INFINITY;                        // not so for weights that are not finite
-      // n maxima: entry i < nblkp is block i of parity 0, then those of parity 1;
-      // or all the labels' scores
-      const bool keep = A.parities == 0;
-      const float* bm = A.bmax + (size_t)b * (keep ? 1 : 2) * A.nblkp;
-      const int n = keep ? (int)A.L : A.nblkp + A.nblk;
-      auto none = [&](int i) { return !keep && i >= A.nblk && i < A.nblkp; };   // padding
+      // n maxima, -inf in the padding between streams; or all the labels' scores
+      const bool keep = A.streams == 0;
+      const float* bm = A.bmax + (size_t)b * (keep ? 1 : kStreams) * A.nblkp;
+      const int n = keep ? (int)A.L : kStreams * A.nblkp;
       auto each = [&](auto f) {
         if (n <= kGroups) {                            // one to a group
           if (tid % (kJoinThreads / kGroups) == 0 && tid / (kJoinThreads / kGroups) < n) {
             const int i = tid / (kJoinThreads / kGroups);
-            if (!none(i)) f(i, __ldcg(bm + i));
+            f(i, __ldcg(bm + i));
           }
         } else if (n <= 4 * kJoinThreads) {
           float v[4];
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const int i = tid + u * kJoinThreads;
-            if (i < n && !none(i)) f(i, v[u]);
+            if (i < n) f(i, v[u]);
           }
         } else {
           const int n4 = (n + 3) / 4;
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
               const float w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (i + e < n && !none(i + e)) f(i + e, w[e]);
+                if (i + e < n) f(i + e, w[e]);
             }
           }
         }
@@ -824,15 +827,15 @@ __global__ void __launch_bounds__(kNearThreads, 2) label_near_kernel(const Args 
   const int lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const int per = A.pairs * tile / kNearAt;
+  const int block = tile / 2, per = A.pairs * block / kNearAt;     // labels of half a tile; warps' shares of a block
   const int64_t work = (int64_t)A.counts->nitems * per;
   for (int64_t w = (int64_t)blockIdx.x * (kNearThreads / 32) + (threadIdx.x >> 5); w < work;
        w += (int64_t)gridDim.x * (kNearThreads / 32)) {
     const int2 it = A.items[w / per];
     const int b = it.x, in = (int)(w % per) * kNearAt;
-    const bool odd = it.y >= A.nblkp;
-    const int64_t pair0 = (int64_t)(odd ? it.y - A.nblkp : it.y) * A.pairs;
-    const int64_t l0 = (2 * (pair0 + in / tile) + odd) * tile + in % tile;
+    const int stream = it.y / A.nblkp;
+    const int64_t pair0 = (int64_t)(it.y % A.nblkp) * A.pairs;
+    const int64_t l0 = (2 * (pair0 + in / block) + (stream >> 1)) * tile + (stream & 1) * block + in % block;
     if (l0 >= A.L) continue;
     int64_t l[kNearAt];
     float z[kNearAt];
@@ -1031,7 +1034,7 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
 
 // ---------------------------------------------------------------- host
 struct Layout {
-  int G, nblk, nblkp, pairs, parities;
+  int G, nblk, nblkp, pairs, streams;
   size_t xa, xb, xinv, n1, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
       rowstat, total;
 };
@@ -1044,13 +1047,13 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   const int P = (B + 127) / 128;
   const int64_t N = tile_labels(h), T = (h->L + N - 1) / N;
   o.pairs = 1;
-  o.parities = k > 0 && h->L <= kKeepLabels && (size_t)B * h->L * 4 <= kKeepBytes ? 0 : 2;
-  if (k > 0 && o.parities)
-    while ((size_t)B * (T / o.pairs) * 4 > kMaxima) o.pairs *= 2;
+  o.streams = k > 0 && h->L <= kKeepLabels && (size_t)B * h->L * 4 <= kKeepBytes ? 0 : kStreams;
+  if (k > 0 && o.streams)
+    while ((size_t)B * (2 * T / o.pairs) * 4 > kMaxima) o.pairs *= 2;
   o.nblk = (int)((T + 2 * o.pairs - 1) / (2 * o.pairs));
   int64_t G = h->num_sms / P;
   if (G > o.nblk) G = o.nblk;
-  if (o.parities == 0) o.nblk = (int)h->L;
+  if (o.streams == 0) o.nblk = (int)h->L;
   o.nblkp = (o.nblk + 7) / 8 * 8;
   if (G < 1) G = 1;
   o.G = (int)G;
@@ -1072,8 +1075,8 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   o.near_v = take(4 * lists * kMaxNear);
   o.near_l = take(4 * lists * kMaxNear);
   o.from = take(4 * lists);
-  o.bmax = take(k > 0 ? (o.parities ? 8 : 4) * (size_t)B * o.nblkp : 0);
-  o.part = take(sizeof(Stat) * (size_t)B * 2 * o.G);
+  o.bmax = take(k > 0 ? 4 * (size_t)(o.streams ? o.streams : 1) * B * o.nblkp : 0);
+  o.part = take(sizeof(Stat) * (size_t)B * kStreams * o.G);
   o.sk = take(8 * (size_t)B * kSegs * k);
   o.si = take(4 * (size_t)B * kSegs * k);
   o.rowstat = take(16 * (size_t)B);
@@ -1120,7 +1123,7 @@ cudaError_t run_join(elmo_head* h, const Args& A, cudaStream_t s) {
   const size_t xbytes = sizeof(float) * (size_t)h->d;
   cudaError_t e = launch_after(label_join_kernel<kFormat>, dim3(A.B), kJoinThreads, xbytes, s, A);
   if (e != cudaSuccess || A.k == 0) return e;
-  if (A.parities != 0) {
+  if (A.streams != 0) {
     e = launch_after(label_near_kernel<kFormat>, dim3(h->num_sms * 4), kNearThreads, 0, s, A, tile_labels(h));
     if (e != cudaSuccess) return e;
   }
@@ -1149,7 +1152,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.label_base = h->label_base;
   A.labels_total = h->labels_total;
   A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.nnz = nnz;
-  A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.parities = o.parities;
+  A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.streams = o.streams;
   A.fmt = w_format(h);
   const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
   A.gamma = (float)nsteps * 0x1p-22f;
@@ -1188,7 +1191,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
     else e = wide ? run_pass<1, 0, 1>(h, A, s) : run_pass<1, 0, 0>(h, A, s);
     if (e != cudaSuccess) return e;
   }
-  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.parities ? 4 : 3);
+  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.streams ? 4 : 3);
   if (A.fmt == ELMO_BF16) return run_join<ELMO_BF16>(h, A, s);
   if (A.fmt == ELMO_FP8_E5M2) return run_join<ELMO_FP8_E5M2>(h, A, s);
   return run_join<ELMO_FP8_E4M3>(h, A, s);
