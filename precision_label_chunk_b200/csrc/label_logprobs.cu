@@ -60,7 +60,6 @@ constexpr int kThreads = 32 * (kEpi + 2);
 constexpr int kMaxStages = 16;
 constexpr uint32_t kAccCol = 384;         // first accumulator column where X lies in TMEM
 constexpr long long kWait = 4000000000LL; // ~2 s
-constexpr float kNoLabel = -3.0e38f;      // a score that e^ takes to 0 and whose product with it is 0
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr size_t kMaxima = size_t(256) << 20;   // bytes of block maxima, about
 constexpr int64_t kKeepLabels = 16384;    // heads of up to so many labels keep every score instead,
@@ -109,7 +108,7 @@ struct Args {
   float* near_v;                          // [B][kMaxNear] their fp32 scores
   int32_t* near_l;
   float* from;                            // [B] the fp32 score from which a label is near
-  Stat* part;                             // [B][kStreams G]
+  Stat* part;                             // [B][kStreams G] reference and sums in powers of two (Soft2)
   uint64_t* seg_key;                      // [B][kSegs][k]
   int32_t* seg_i;
   const int32_t *rowptr, *cols;
@@ -204,6 +203,7 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
 // ---------------------------------------------------------------- 2. score pass
 struct SmemP {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+  float win[8][32 * 4 * kStreams];
   uint32_t tmem_base;
   int abort;
 };
@@ -382,19 +382,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, r = quad * 32 + lane, row = p * 128 + r;
     const bool live = row < A.B;
     const float inv = live ? A.xinv[row] : 1.0f;       // scores are inv times the accumulators
-    Soft soft(inv);
-    const bool keep = A.k > 0 && A.streams == 0;
+    Soft2 soft(inv);
+    const float no_label = -1.0e30f / soft.c2;         // a score that 2^ takes to 0
+    const bool keep = A.k > 0 && A.streams == 0, lists = A.k > 0 && !keep && live;
     float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * kStreams + stream) * A.nblkp;
-    float win[8];                                      // maxima of the aligned eight blocks under way
-#pragma unroll
-    for (int e = 0; e < 8; ++e) win[e] = -INFINITY;
+    // maxima of the aligned eight blocks under way, a column of shared memory a thread
+    float* win = S->win[0] + (warp - 2) * 32 + lane;
+    const int L = (int)A.L, last = (int)t1;
     uint32_t nt = 0;
     bool ok = true;
-    for (int64_t blk = blk0; blk < blk1 && ok; ++blk) {
+    int tile = (int)t0 + par;
+    for (int blk = (int)blk0; blk < (int)blk1 && ok; ++blk) {
       float best = -INFINITY;
-      for (int i = 0; i < A.pairs; ++i) {
-        const int64_t tile = 2 * (blk * A.pairs + i) + par;
-        if (tile >= t1) break;
+      for (int i = 0; i < A.pairs && tile < last; ++i, tile += 2) {
         if (!mbar_wait(&S->tfull[par], nt & 1, abort, kWait)) { record_timeout(A.status, abort, 74); ok = false; break; }
         ++nt;
         tc_fence_after();
@@ -409,19 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S->tempty[par]);
           }
-          const int64_t l0 = tile * kN + half * (kN / 2) + u * 32;
-          if (!live || l0 >= A.L) continue;
+          const int l0 = tile * kN + half * (kN / 2) + u * 32;
+          if (!live || l0 >= L) continue;
           float v[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[c]);
-          if (l0 + 32 > A.L) {                         // past the end there are no labels
+          if (l0 + 32 > L) {                           // past the end there are no labels
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (l0 + c >= A.L) v[c] = kNoLabel;
+              if (l0 + c >= L) v[c] = no_label;
           }
           const float mx = max32(v);
           best = fmaxf(best, mx);
-          soft.add32<false>(v, mx);
+          soft.add32(v, mx);
           if (keep) {
 #pragma unroll
             for (int c = 0; c < 32; c += 4)
@@ -429,27 +429,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (A.k > 0 && !keep && live) {
-        const int j = (int)blk & 7;
+      if (lists) {
+        const int j = blk & 7;
+        win[j * 32 * 4 * kStreams] = best;
+        if (j == 7 || blk + 1 == (int)blk1) {
+          const bool end = blk + 1 == A.nblk;          // of the row: the padding holds nothing
+          const int first = blk - j;
+          float w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) win[e] = e == j ? best : win[e];
-        const bool end = blk + 1 == A.nblk;            // of the row: the padding holds nothing
-        if (j == 7 || blk + 1 == blk1) {
-          const int64_t first = blk - j;
-          if (first >= blk0 && (j == 7 || end)) {
-            reinterpret_cast<float4*>(bm + first)[0] = make_float4(win[0], win[1], win[2], win[3]);
-            reinterpret_cast<float4*>(bm + first)[1] = make_float4(win[4], win[5], win[6], win[7]);
+          for (int e = 0; e < 8; ++e) w[e] = e <= j ? win[e * 32 * 4 * kStreams] : -INFINITY;
+          if (first >= (int)blk0 && (j == 7 || end)) {
+            reinterpret_cast<float4*>(bm + first)[0] = make_float4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<float4*>(bm + first)[1] = make_float4(w[4], w[5], w[6], w[7]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if ((e <= j || end) && first + e >= blk0) bm[first + e] = win[e];
+              if ((e <= j || end) && first + e >= (int)blk0) bm[first + e] = w[e];
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) win[e] = -INFINITY;
         }
       }
     }
-    if (live) A.part[((size_t)row * A.G + g) * kStreams + stream] = {soft.m * inv, soft.s, soft.t * inv};
+    if (live)
+      A.part[((size_t)row * A.G + g) * kStreams + stream] = {soft.m > -INFINITY ? soft.r : -INFINITY, soft.s, soft.t};
   } else if (scan) {
     // bf16 magnitudes by 16-bit maxima, two instructions for two weights.  Of
     // 8-bit magnitudes x, x + (0x7F - m) carries into the sign bit exactly
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (q[i].m == -INFINITY) { s += q[i].s; continue; }
-      const double d = (double)q[i].m - (double)mf, c = q[i].m == mf ? 1.0 : exp(d);
+      const double d = (double)q[i].m - (double)mf, c = q[i].m == mf ? 1.0 : exp2(d);
       s += c * q[i].s;
       t += c * (q[i].t + (q[i].m == mf ? 0.0 : d * q[i].s));
     }
@@ -692,7 +693,8 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
     if (tid == 0) {
       s = t = 0.0;
       for (int w = 0; w < kW; ++w) { s += ws[w]; t += wt[w]; }
-      double m = mf, logs = log(s), lse = m + logs, H = logs - t / s;
+      constexpr double kLn2 = 0.693147180559945309417;
+      double m = mf * kLn2, logs = log(s), lse = m + logs, H = logs - t / s * kLn2;
       if (mf == -INFINITY) {                           // no label has a finite score
         lse = s == 0.0 ? -INFINITY : NAN;
         H = s == 0.0 ? 0.0 : NAN;

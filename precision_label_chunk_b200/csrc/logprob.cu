@@ -162,7 +162,7 @@ __device__ __forceinline__ float add_raw(Soft& soft, const Raw<float>& r) {
     v[4 * i + 3] = __uint_as_float(r.q[i].w);
   }
   const float mx = max32(v);
-  soft.add32<true>(v, mx);
+  soft.add32(v, mx);
   return mx;
 }
 __device__ __forceinline__ float add_raw(Soft& soft, const Raw<uint16_t>& r) {
@@ -183,7 +183,7 @@ __device__ __forceinline__ float add_raw(Soft& soft, const Raw<uint16_t>& r) {
   if (mx > soft.m) soft.raise(mx);
   const float m0 = soft.m > -INFINITY ? soft.m : 0.0f;
   float ss, tt;
-  soft.sums32_of([&](int c) { return minus_f32(max_nan_bf16x2(w[c], 0xFF7FFF7Fu), m0); }, ss, tt);
+  soft.sums32([&](int c) { return minus_f32(max_nan_bf16x2(w[c], 0xFF7FFF7Fu), m0); }, ss, tt);
   if (tt != tt || m0 < -1.0e38f) {
     float v[32];
 #pragma unroll
@@ -209,7 +209,7 @@ template <int kW, typename T>
 __device__ __forceinline__ Stat scan_blocks(const Args& A, const T* z, int64_t b, int blk0, int blk1, SmemS<kW>* S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int shift = shift_of(z);
-  Soft soft(1.0f);
+  Soft soft;
   Raw<T> next;
   int blk = blk0 + warp;
   if (blk < blk1) next = load_raw(z, A.L, (int64_t)blk * kBlock - shift, lane);
@@ -228,7 +228,7 @@ __device__ __forceinline__ Stat scan_blocks(const Args& A, const T* z, int64_t b
   __syncthreads();                                     // the last segment's sums are read
   if (lane == 0) S->row[warp] = {soft.m, soft.s, soft.t};
   __syncthreads();
-  Soft all(1.0f);
+  Soft all;
   if (lane < kW) { all.m = S->row[lane].m; all.s = S->row[lane].s; all.t = S->row[lane].t; }
   all.join_warp();
   return {all.m, all.s, all.t};

@@ -46,65 +46,58 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   return r;
 }
 
+// max of three in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ float max32(const float (&v)[32]) {
-  float x[8];
+  float x[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-  for (int c = 0; c < 8; ++c) x[c] = fmaxf(fmaxf(v[c], v[c + 8]), fmaxf(v[c + 16], v[c + 24]));
-  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  for (int c = 4; c < 28; c += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = max3(x[e], v[c + e], v[c + 4 + e]);
+  return max3(max3(x[0], x[1], x[2]), max3(x[3], v[28], v[29]), fmaxf(v[30], v[31]));
 }
 
 // Partial sums of a row's softmax: m its maximum, s = sum e^(z - m),
 // t = sum e^(z - m)(z - m).
 struct Stat { float m, s, t; };
 
-// A thread's running m, s and t over values v whose scores are inv v; m and t
-// are in the values' units (inv m, inv t are the scores').  About 4 issue
-// slots a value (5 with kMasks), one of them for the exponential.
+// A thread's running m, s and t over scores.  About 5 issue slots a score, one
+// of them for the exponential.
 struct Soft {
   float m = -INFINITY, s = 0.0f, t = 0.0f;
-  float c2, floor_v;                                   // inv log2(e); -200 / inv
-
-  __device__ __forceinline__ explicit Soft(float inv) : c2(inv * kLog2e), floor_v(kSoftFloor / inv) {}
 
   __device__ __forceinline__ void raise(float to) {    // m <- to, to >= m
     if (m > -INFINITY) {
-      const float dm = fmaxf(m - to, floor_v), c = ex2(dm * c2);
+      const float dm = fmaxf(m - to, kSoftFloor), c = ex2(dm * kLog2e);
       t = c * fmaf(s, dm, t);
       s *= c;
     }
     m = to;
   }
 
-  // 32 values with the maximum mx.  kMasks: values of -inf are ordinary (they
-  // are cut at the floor, where e^ is 0); else they are rare, and a product 0
-  // times infinity sends the 32 values through the sums again (add32_slow).
-  template <bool kMasks>
+  // 32 scores with the maximum mx; -inf is cut at the floor, where e^ is 0
   __device__ __forceinline__ void add32(const float (&v)[32], float mx) {
     if (mx > m) raise(mx);
     const float m0 = m > -INFINITY ? m : 0.0f;
+    const f2 nm = pair(-m0, -m0);
     float ss, tt;
-    sums32<kMasks>(v, m0, ss, tt);
-    if (!kMasks && tt != tt) slow32(v, m0, ss, tt);
+    sums32([&](int c) {
+      float a, b;
+      unpair(add2(pair(v[2 * c], v[2 * c + 1]), nm), a, b);
+      return pair(max_nan(a, kSoftFloor), max_nan(b, kSoftFloor));
+    }, ss, tt);
     s += ss;
     t += tt;
   }
-  template <bool kMasks>
-  __device__ __forceinline__ void sums32(const float (&v)[32], float m0, float& ss, float& tt) const {
-    const f2 nm = pair(-m0, -m0);
-    sums32_of([&](int c) {
-      f2 d = add2(pair(v[2 * c], v[2 * c + 1]), nm);
-      if (kMasks) {
-        float a, b;
-        unpair(d, a, b);
-        d = pair(max_nan(a, floor_v), max_nan(b, floor_v));
-      }
-      return d;
-    }, ss, tt);
-  }
-  // sums over the 16 pairs of differences v - m that diff(c) gives
+  // sums over the 16 pairs of differences z - m that diff(c) gives
   template <typename F>
-  __device__ __forceinline__ void sums32_of(F diff, float& ss, float& tt) const {
-    const f2 cc = pair(c2, c2);
+  __device__ __forceinline__ void sums32(F diff, float& ss, float& tt) const {
+    const f2 cc = pair(kLog2e, kLog2e);
     f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
@@ -125,7 +118,7 @@ struct Soft {
     ss = tt = 0.0f;
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      const float d = max_nan(v[c] - m0, floor_v), e = ex2(d * c2);
+      const float d = max_nan(v[c] - m0, kSoftFloor), e = ex2(d * kLog2e);
       ss += e;
       tt = fmaf(e, d, tt);
     }
@@ -140,6 +133,60 @@ struct Soft {
       s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
       t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
+  }
+};
+
+// The same over accumulators v of scores inv v, in powers of two: with
+// c2 = inv log2(e) and a reference r = fl(c2 max v),
+//     s = sum 2^(c2 v - r),   t = sum 2^(c2 v - r)(c2 v - r),
+// so that a value takes one multiply-add, the exponential, an addition and a
+// multiply-add, two values an instruction but for the exponential.  The score
+// that r stands for is r ln 2 without a rounding, whatever c2 max v rounded
+// to; c2 v - r is rounded once, to within 2^-24 of its size: c2 itself is off
+// by 2^-25, which moves a score by as much of itself, a quarter of what an
+// accumulation in fp32 may.
+struct Soft2 {
+  float m = -INFINITY, r = 0.0f, s = 0.0f, t = 0.0f;
+  float c2;
+
+  __device__ __forceinline__ explicit Soft2(float inv) : c2(inv * kLog2e) {}
+
+  __device__ __forceinline__ void add32(const float (&v)[32], float mx) {
+    if (mx > m) {
+      const float to = mx * c2;
+      if (m > -INFINITY) {
+        const float d = fmaxf(r - to, -300.0f), c = ex2(d);
+        t = c * fmaf(s, d, t);
+        s *= c;
+      }
+      m = mx;
+      r = to;
+    }
+    const f2 cc = pair(c2, c2), nr = pair(-r, -r);
+    f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const f2 d = fma2(pair(v[2 * c], v[2 * c + 1]), cc, nr);
+      float a, b;
+      unpair(d, a, b);
+      const f2 e = pair(ex2(a), ex2(b));
+      ps[c & 1] = add2(ps[c & 1], e);
+      pt[c & 1] = fma2(e, d, pt[c & 1]);
+    }
+    float s0, s1, t0, t1;
+    unpair(add2(ps[0], ps[1]), s0, s1);
+    unpair(add2(pt[0], pt[1]), t0, t1);
+    float tt = t0 + t1;
+    if (tt != tt) {                                    // a score of -inf (0 times infinity), or a NaN
+      tt = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float d = max_nan(fmaf(v[c], c2, -r), -300.0f);
+        tt = fmaf(ex2(d), d, tt);
+      }
+    }
+    s += s0 + s1;
+    t += tt;
   }
 };
 
