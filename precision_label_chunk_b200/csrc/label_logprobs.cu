@@ -58,7 +58,7 @@ constexpr int kStreams = 4;               // groups of four epilogue warps: even
 constexpr int kEpi = 2 + 4 * kStreams;    // warp 0 TMA, 1 MMA and TMEM, 2 .. kEpi - 1 epilogue, then two for max|W|
 constexpr int kThreads = 32 * (kEpi + 2);
 constexpr int kMaxStages = 16;
-constexpr uint32_t kAccCol = 384;         // first accumulator column where X lies in TMEM
+constexpr int kMaxBufs = 4;               // accumulators
 constexpr long long kWait = 4000000000LL; // ~2 s
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr size_t kMaxima = size_t(256) << 20;   // bytes of block maxima, about
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
 
 // ---------------------------------------------------------------- 2. score pass
 struct SmemP {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[kMaxBufs], tempty[kMaxBufs];
   float win[8][32 * 4 * kStreams];
   uint32_t tmem_base;
   int abort;
@@ -214,9 +214,12 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
 }
 
 // kFp8: 8-bit head (kW5: E5M2 weights).  kXs = 0: d <= 768, X (two 8-bit or
-// one bf16 operand, 2 d bytes a query) stays in TMEM columns 0..383 and tiles
-// are 64 labels with two accumulators in the rest; kXs = 1: wider heads, X
-// comes through the ring with W, tiles are 128 labels.
+// one bf16 operand, 2 d bytes a query) stays in the first TMEM columns, d / 2
+// of the 512, and tiles are 64 labels; kXs = 1: wider heads, X comes through
+// the ring with W, tiles are 128 labels.  The last columns hold four
+// accumulators, two where X takes more than half: handing one over and back
+// takes about 0.75 us, which two hide only behind a long tile (1M labels x
+// 256, 105 queries: 87 us with two).
 //
 // A stage of the ring holds kbs 128-byte k-blocks of q tiles, up to 48 KB in
 // one TMA request: the rate of the copies follows the number of requests (the
@@ -244,12 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nkb = (A.d + kKE - 1) / kKE;
   const int nst = (nkb + A.kbs - 1) / A.kbs;           // stages of a group of q tiles (1 where q > 1)
   const uint32_t opcols = (uint32_t)nkb * 32;
+  const uint32_t nbuf = kXs || kOps * opcols <= 256 ? 4 : 2, acc0 = 512 - nbuf * kN;   // the accumulators' first column
+  const uint32_t bufs = nbuf - 1, bufs_log = nbuf >> 1;                               // rel & bufs, rel >> bufs_log
   volatile int* abort = &S->abort;
   const bool scan = A.k > 0;                           // the ranges are scanned for max|W|
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < A.stages; ++s) { mbar_init(&S->full[s], 1); mbar_init(&S->empty[s], scan ? 3 : 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 8); }
+    for (int i = 0; i < kMaxBufs; ++i) { mbar_init(&S->tfull[i], 1); mbar_init(&S->tempty[i], 8); }
     S->abort = 0;
     fence_barrier_init();
   }
@@ -333,17 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t ws = smem_u32(ring + (size_t)s * stage);
           for (int j = 0; j < A.q && t + j < t1; ++j) {
-            const int64_t rel = t + j - t0;
-            const uint32_t buf = (uint32_t)rel & 1;
+            const uint32_t rel = (uint32_t)(t + j - t0), buf = rel & bufs;
             if (st == 0) {
-              if (!mbar_wait(&S->tempty[buf], (uint32_t)((rel >> 1) & 1) ^ 1, abort, kWait)) {
+              if (!mbar_wait(&S->tempty[buf], ((rel >> bufs_log) & 1) ^ 1, abort, kWait)) {
                 record_timeout(A.status, abort, 72);
                 ok = false;
                 break;
               }
               tc_fence_after();
             }
-            const uint32_t dcol = tmem + (kXs ? 0 : kAccCol) + buf * kN;
+            const uint32_t dcol = tmem + acc0 + buf * kN;
             for (int i = 0; i < A.kbs && st * A.kbs + i < nkb; ++i) {
               const int kb = st * A.kbs + i;
               const uint32_t wk = ws + (uint32_t)i * slab + (uint32_t)j * (kN * 128);
@@ -389,25 +393,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // maxima of the aligned eight blocks under way, a column of shared memory a thread
     float* win = S->win[0] + (warp - 2) * 32 + lane;
     const int L = (int)A.L, last = (int)t1;
-    uint32_t nt = 0;
+    uint32_t rel = par;
     bool ok = true;
     int tile = (int)t0 + par;
     for (int blk = (int)blk0; blk < (int)blk1 && ok; ++blk) {
       float best = -INFINITY;
-      for (int i = 0; i < A.pairs && tile < last; ++i, tile += 2) {
-        if (!mbar_wait(&S->tfull[par], nt & 1, abort, kWait)) { record_timeout(A.status, abort, 74); ok = false; break; }
-        ++nt;
+      for (int i = 0; i < A.pairs && tile < last; ++i, tile += 2, rel += 2) {
+        const uint32_t buf = rel & bufs;
+        if (!mbar_wait(&S->tfull[buf], (rel >> bufs_log) & 1, abort, kWait)) {
+          record_timeout(A.status, abort, 74);
+          ok = false;
+          break;
+        }
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < kN / 64; ++u) {
           __syncwarp();
           uint32_t raw[32];
-          tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + (kXs ? 0 : kAccCol) + par * kN + half * (kN / 2) + u * 32, raw);
+          tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + acc0 + buf * kN + half * (kN / 2) + u * 32, raw);
           tmem_wait_ld();
           if (u == kN / 64 - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S->tempty[par]);
+            if (lane == 0) mbar_arrive(&S->tempty[buf]);
           }
           const int l0 = tile * kN + half * (kN / 2) + u * 32;
           if (!live || l0 >= L) continue;
