@@ -213,6 +213,47 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   if (atomicCAS(status, 0, (int)ELMO_ETIMEOUT) == 0) status[1] = site;
 }
 
+// Four MMAs along K, 32 bytes each (D += A B, the first D = A B unless `more`),
+// A in tensor memory or in shared memory.  One thread issues them all, each of
+// its instructions waiting for the one before, so that an MMA of 64 labels,
+// 32 clocks of the tensor pipe, went out every 60 while its descriptor was
+// formed anew: here only the addresses move on.
+#define ELMO_MMA4(KIND, A_OPERAND)                                                          \
+  "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("%1") ", %2, %3, p;\n\t"       \
+  "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("a1") ", b1, %3, q;\n\t"       \
+  "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("a2") ", b2, %3, q;\n\t"       \
+  "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("a3") ", b3, %3, q;\n\t}"
+#define ELMO_MMA4_HEAD(A_BITS, A_STEP1, A_STEP2, A_STEP3)                                   \
+  "{\n\t.reg .pred p, q;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b" A_BITS " a1, a2, a3;\n\t"     \
+  "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                       \
+  "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"                      \
+  "add.u" A_BITS " a1, %1, " A_STEP1 ";\n\tadd.u" A_BITS " a2, %1, " A_STEP2 ";\n\t"        \
+  "add.u" A_BITS " a3, %1, " A_STEP3 ";\n\t"
+#define ELMO_A_TMEM(R) "[" R "]"
+#define ELMO_A_SMEM(R) R
+template <int kFp8>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more) {
+  if constexpr (kFp8)
+    asm volatile(ELMO_MMA4_HEAD("32", "8", "16", "24") ELMO_MMA4("f8f6f4", ELMO_A_TMEM)
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+  else
+    asm volatile(ELMO_MMA4_HEAD("32", "8", "16", "24") ELMO_MMA4("f16", ELMO_A_TMEM)
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+}
+template <int kFp8>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more) {
+  if constexpr (kFp8)
+    asm volatile(ELMO_MMA4_HEAD("64", "2", "4", "6") ELMO_MMA4("f8f6f4", ELMO_A_SMEM)
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+  else
+    asm volatile(ELMO_MMA4_HEAD("64", "2", "4", "6") ELMO_MMA4("f16", ELMO_A_SMEM)
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(more) : "memory");
+}
+#undef ELMO_MMA4
+#undef ELMO_MMA4_HEAD
+#undef ELMO_A_TMEM
+#undef ELMO_A_SMEM
+
 // kFp8: 8-bit head (kW5: E5M2 weights).  kXs = 0: d <= 768, X (two 8-bit or
 // one bf16 operand, 2 d bytes a query) stays in the first TMEM columns, d / 2
 // of the 512, and tiles are 64 labels; kXs = 1: wider heads, X comes through
@@ -336,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int st = 0; st < nst && ok; ++st) {
           if (!mbar_wait(&S->full[s], ph, abort, kWait)) { record_timeout(A.status, abort, 73); ok = false; break; }
           tc_fence_after();
-          const uint32_t ws = smem_u32(ring + (size_t)s * stage);
+          // descriptors advance by their start addresses, in units of 16 bytes
+          const uint64_t wd = sw128_desc(smem_u32(ring + (size_t)s * stage), 16, 1024), xd = wd + (wbytes >> 4);
           for (int j = 0; j < A.q && t + j < t1; ++j) {
             const uint32_t rel = (uint32_t)(t + j - t0), buf = rel & bufs;
             if (st == 0) {
@@ -350,23 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dcol = tmem + acc0 + buf * kN;
             for (int i = 0; i < A.kbs && st * A.kbs + i < nkb; ++i) {
               const int kb = st * A.kbs + i;
-              const uint32_t wk = ws + (uint32_t)i * slab + (uint32_t)j * (kN * 128);
+              const uint64_t bd = wd + (((uint32_t)i * slab + (uint32_t)j * (kN * 128)) >> 4);
 #pragma unroll
-              for (int op = 0; op < kOps; ++op) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {          // 32 bytes of K an instruction
-                  const uint64_t bd = sw128_desc(wk + k * 32, 16, 1024);
-                  const uint32_t more = (kb | op | k) != 0;
-                  if (kXs) {
-                    const uint64_t ad = sw128_desc(ws + wbytes + (uint32_t)(op * A.kbs + i) * 16384 + k * 32, 16, 1024);
-                    if (kFp8) mma_e4m3(dcol, ad, bd, idesc[op], more);
-                    else mma_bf16(dcol, ad, bd, idesc[0], more);
-                  } else {
-                    const uint32_t a = tmem + (uint32_t)op * opcols + (uint32_t)kb * 32 + (uint32_t)k * 8;
-                    if (kFp8) mma_e4m3_ts(dcol, a, bd, idesc[op], more);
-                    else mma_bf16_ts(dcol, a, bd, idesc[0], more);
-                  }
-                }
+              for (int op = 0; op < kOps; ++op) {      // four instructions of 32 bytes of K
+                const uint32_t more = (kb | op) != 0;
+                if (kXs) mma4_ss<kFp8>(dcol, xd + (uint32_t)(op * A.kbs + i) * (16384 >> 4), bd, idesc[op], more);
+                else mma4_ts<kFp8>(dcol, tmem + (uint32_t)op * opcols + (uint32_t)kb * 32, bd, idesc[op], more);
               }
             }
             if (st == nst - 1) mma_commit(&S->tfull[buf]);
