@@ -665,6 +665,67 @@ __device__ __forceinline__ float two_delta(const Args& A, int b) {
   return __fmul_ru(2.0f, __fadd_ru(d, 0x1p-126f));
 }
 
+// Ranks a query's `near` labels near the k-th best by exact scores, or lists the
+// query for the exact path.  The whole CTA.
+struct SmemR {
+  double ex[kMaxExact];
+  int32_t el[kMaxExact];
+  int nexact;
+};
+
+template <int kFormat, int kThr>
+__device__ __forceinline__ void rank_near(const Args& A, int b, const float* xs, int near, double m, double logs, SmemB* S,
+                                          SmemR* R) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  bool ok = near >= A.k && near <= kMaxNear;
+  const float* nv = A.near_v + (size_t)b * kMaxNear;
+  if (tid == 0) R->nexact = 0;
+  if (ok) {
+    const float two = two_delta(A, b);
+    float best = -INFINITY;
+    for (int i = tid; i < near; i += kThr) best = fmaxf(best, nv[i]);
+    const float cut = __fsub_rd(lower_bound_kth<kThr>(S, best, A.k), two);
+    for (int i = tid; i < near; i += kThr) {
+      if (nv[i] >= cut) {
+        const int at = atomicAdd(&R->nexact, 1);
+        if (at < kMaxExact) R->el[at] = A.near_l[(size_t)b * kMaxNear + i];
+      }
+    }
+    __syncthreads();
+    ok = R->nexact <= kMaxExact;
+  }
+  if (!ok) {
+    if (tid == 0) A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
+    return;
+  }
+  const int n = R->nexact;
+  for (int i = warp; i < n; i += kThr / 32) {
+    const double z = exact_score<kFormat>(xs, A.W, R->el[i], A.d, lane);
+    if (lane == 0) R->ex[i] = z;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThr) {
+    const double z = R->ex[i];
+    const int32_t l = R->el[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += R->ex[j] > z || (R->ex[j] == z && R->el[j] < l);
+    if (rank < A.k) {
+      A.top_idx[(size_t)b * A.k + rank] = (int32_t)(l + A.label_base);
+      A.top_logp[(size_t)b * A.k + rank] = (float)(z - m - logs);
+    }
+  }
+}
+
+// A query as fp32 numbers in shared memory.
+template <int kThr>
+__device__ __forceinline__ void load_query(const Args& A, int b, float* xs) {
+  for (int j = threadIdx.x; j < A.d / 2; j += kThr) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(A.X + (size_t)b * A.d)[j];
+    xs[2 * j] = __uint_as_float(w << 16);
+    xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+}
+
 // Statistics of a query, log p of its given labels, and the blocks that may
 // hold its k best labels.
 template <int kFormat>
@@ -672,6 +733,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   extern __shared__ __align__(16) uint8_t dyn[];
   float* xs = reinterpret_cast<float*>(dyn);           // [d] the query
   __shared__ SmemB S;
+  __shared__ SmemR R;
   __shared__ int32_t blocks[kMaxBlocks];
   constexpr int kW = kJoinThreads / 32;
   constexpr int kEarly = 512;
@@ -679,11 +741,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   __shared__ float wm[kW];
   __shared__ int nblocks, at0;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int j = tid; j < A.d / 2; j += kJoinThreads) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(A.X + (size_t)b * A.d)[j];
-    xs[2 * j] = __uint_as_float(w << 16);
-    xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
-  }
+  load_query<kJoinThreads>(A, b, xs);
   if (tid == 0) nblocks = 0;
   __syncthreads();
   // the given labels' scores need only X and W: the first kEarly of them while
@@ -828,15 +886,14 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
         A.listed[b] = ok;
         if (!ok) {
           A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
-        } else if (keep) {
-          A.nnear[b] = found;
-        } else {
+        } else if (!keep) {
           at0 = atomicAdd(&A.counts->nitems, found);
           A.from[b] = __fsub_rd(__fmul_rd(low, inv), two);
         }
       }
       __syncthreads();
-      if (ok && !keep)
+      if (ok && keep) rank_near<kFormat, kJoinThreads>(A, b, xs, found, m, logs, &S, &R);
+      else if (ok)
         for (int i = tid; i < found; i += kJoinThreads) A.items[at0 + i] = make_int2(b, blocks[i]);
     }
   }
@@ -902,58 +959,13 @@ __global__ void __launch_bounds__(kNearThreads) label_rank_kernel(const Args A) 
   extern __shared__ __align__(16) uint8_t dyn[];
   float* xs = reinterpret_cast<float*>(dyn);           // [d]
   __shared__ SmemB S;
-  __shared__ double ex[kMaxExact];
-  __shared__ int32_t el[kMaxExact];
-  __shared__ int nexact;
-  constexpr int kW = kNearThreads / 32;
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int j = tid; j < A.d / 2; j += kNearThreads) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(A.X + (size_t)b * A.d)[j];
-    xs[2 * j] = __uint_as_float(w << 16);
-    xs[2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
-  }
-  if (tid == 0) nexact = 0;
+  __shared__ SmemR R;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  load_query<kNearThreads>(A, b, xs);
   pdl_wait();
   pdl_trigger();
-  if (A.listed[b] == 0) return;                          // answered, or a failed query already
-  const int near = A.nnear[b];
-  bool ok = near >= A.k && near <= kMaxNear;
-  const float* nv = A.near_v + (size_t)b * kMaxNear;
-  if (ok) {
-    const float two = two_delta(A, b);
-    float best = -INFINITY;
-    for (int i = tid; i < near; i += kNearThreads) best = fmaxf(best, nv[i]);
-    const float cut = __fsub_rd(lower_bound_kth<kNearThreads>(&S, best, A.k), two);
-    for (int i = tid; i < near; i += kNearThreads) {
-      if (nv[i] >= cut) {
-        const int at = atomicAdd(&nexact, 1);
-        if (at < kMaxExact) el[at] = A.near_l[(size_t)b * kMaxNear + i];
-      }
-    }
-    __syncthreads();
-    ok = nexact <= kMaxExact;
-  }
-  if (!ok) {
-    if (tid == 0) A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
-    return;
-  }
-  const int n = nexact;
-  for (int i = warp; i < n; i += kW) {
-    const double z = exact_score<kFormat>(xs, A.W, el[i], A.d, lane);
-    if (lane == 0) ex[i] = z;
-  }
-  __syncthreads();
-  const double m = A.rowstat[2 * b], logs = A.rowstat[2 * b + 1];
-  for (int i = tid; i < n; i += kNearThreads) {
-    const double z = ex[i];
-    const int32_t l = el[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += ex[j] > z || (ex[j] == z && el[j] < l);
-    if (rank < A.k) {
-      A.top_idx[(size_t)b * A.k + rank] = (int32_t)(l + A.label_base);
-      A.top_logp[(size_t)b * A.k + rank] = (float)(z - m - logs);
-    }
-  }
+  if (A.listed[b] == 0) return;                        // answered, or a failed query already
+  rank_near<kFormat, kNearThreads>(A, b, xs, A.nnear[b], A.rowstat[2 * b], A.rowstat[2 * b + 1], &S, &R);
 }
 
 // ---------------------------------------------------------------- 4. exact path
@@ -1167,9 +1179,9 @@ cudaError_t run_join(elmo_head* h, const Args& A, cudaStream_t s) {
   if (A.streams != 0) {
     e = launch_after(label_near_kernel<kFormat>, dim3(h->num_sms * 4), kNearThreads, 0, s, A, tile_labels(h));
     if (e != cudaSuccess) return e;
+    e = launch_after(label_rank_kernel<kFormat>, dim3(A.B), kNearThreads, xbytes, s, A);
+    if (e != cudaSuccess) return e;
   }
-  e = launch_after(label_rank_kernel<kFormat>, dim3(A.B), kNearThreads, xbytes, s, A);
-  if (e != cudaSuccess) return e;
   return launch_after(label_exact_kernel<kFormat>, dim3(h->num_sms * 2), kExactThreads, xbytes, s, A);
 }
 
@@ -1232,7 +1244,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
     else e = wide ? run_pass<1, 0, 1>(h, A, s) : run_pass<1, 0, 0>(h, A, s);
     if (e != cudaSuccess) return e;
   }
-  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.streams ? 4 : 3);
+  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.streams ? 4 : 2);
   if (A.fmt == ELMO_BF16) return run_join<ELMO_BF16>(h, A, s);
   if (A.fmt == ELMO_FP8_E5M2) return run_join<ELMO_FP8_E5M2>(h, A, s);
   return run_join<ELMO_FP8_E4M3>(h, A, s);
