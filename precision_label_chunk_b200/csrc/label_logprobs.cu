@@ -418,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = row < A.B;
     const float inv = live ? A.xinv[row] : 1.0f;       // scores are inv times the accumulators
     Soft2 soft(inv);
-    const float no_label = -1.0e30f / soft.c2;         // a score that 2^ takes to 0
     const bool keep = A.k > 0 && A.streams == 0, lists = A.k > 0 && !keep && live;
     float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * kStreams + stream) * A.nblkp;
     // maxima of the aligned eight blocks under way, a column of shared memory a thread
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (l0 + 32 > L) {                           // past the end there are no labels
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (l0 + c >= L) v[c] = no_label;
+              if (l0 + c >= L) v[c] = -INFINITY;
           }
           const float mx = max32(v);
           best = fmaxf(best, mx);
@@ -814,14 +813,15 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   const double m = stat[0], logs = stat[1];
 
   if (A.k > 0) {
-    if (bad) {
+    const float two = two_delta(A, b), inv = A.xinv[b];
+    if (bad || (A.n1[b] == 0.0f && A.r1[b] == 0.0f && two < INFINITY)) {
+      // no list, or that of a query of zeros (as padding is): every label's score is 0
       if (tid == 0) A.listed[b] = 0;
       for (int i = tid; i < A.k; i += kJoinThreads) {
-        A.top_idx[(size_t)b * A.k + i] = -1;
-        A.top_logp[(size_t)b * A.k + i] = -INFINITY;
+        A.top_idx[(size_t)b * A.k + i] = bad ? -1 : (int32_t)(i + A.label_base);
+        A.top_logp[(size_t)b * A.k + i] = bad ? -INFINITY : (float)(0.0 - m - logs);
       }
     } else {
-      const float two = two_delta(A, b), inv = A.xinv[b];
       bool ok = two < INFINITY;                        // not so for weights that are not finite
       // n maxima, -inf in the padding between streams; or all the labels' scores
       const bool keep = A.streams == 0;

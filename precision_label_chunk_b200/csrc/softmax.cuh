@@ -144,8 +144,12 @@ struct Soft {
 // that r stands for is r ln 2 without a rounding, whatever c2 max v rounded
 // to; c2 v - r is rounded once, to within 2^-24 of its size: c2 itself is off
 // by 2^-25, which moves a score by as much of itself, a quarter of what an
-// accumulation in fp32 may.
+// accumulation in fp32 may.  Where |r| passes kFar that rounding of r would
+// reach the exponentials' range: there the differences are taken first, one by
+// one, and r stands for the maximum itself, to within 2^-24 of it.
 struct Soft2 {
+  static constexpr float kFar = 1048576.0f;
+
   float m = -INFINITY, r = 0.0f, s = 0.0f, t = 0.0f;
   float c2;
 
@@ -155,7 +159,7 @@ struct Soft2 {
     if (mx > m) {
       const float to = mx * c2;
       if (m > -INFINITY) {
-        const float d = fmaxf(r - to, -300.0f), c = ex2(d);
+        const float d = fmaxf(fabsf(to) > kFar || fabsf(r) > kFar ? (m - mx) * c2 : r - to, -300.0f), c = ex2(d);
         t = c * fmaf(s, d, t);
         s *= c;
       }
@@ -176,16 +180,19 @@ struct Soft2 {
     float s0, s1, t0, t1;
     unpair(add2(ps[0], ps[1]), s0, s1);
     unpair(add2(pt[0], pt[1]), t0, t1);
-    float tt = t0 + t1;
-    if (tt != tt) {                                    // a score of -inf (0 times infinity), or a NaN
-      tt = 0.0f;
+    float ss = s0 + s1, tt = t0 + t1;
+    const bool far = fabsf(r) > kFar;
+    if (tt != tt || far) {                             // also a score of -inf (0 times infinity), or a NaN
+      ss = tt = 0.0f;
+      const float m0 = m > -INFINITY ? m : 0.0f;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        const float d = max_nan(fmaf(v[c], c2, -r), -300.0f);
-        tt = fmaf(ex2(d), d, tt);
+        const float d = max_nan(far ? (v[c] - m0) * c2 : fmaf(v[c], c2, -r), -300.0f), e = ex2(d);
+        ss += e;
+        tt = fmaf(e, d, tt);
       }
     }
-    s += s0 + s1;
+    s += ss;
     t += tt;
   }
 };

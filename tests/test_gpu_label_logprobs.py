@@ -120,6 +120,47 @@ def test_odd_queries(grid, d):
     h.close()
 
 
+@pytest.mark.parametrize("grid,L,d", [("e4m3", 300_001, 128), ("bf16", 3001, 832), ("e5m2", 40_000, 64)])
+def test_padded_batches(grid, L, d):
+    """Queries of zeros among the others, and queries that belong to nobody's list."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L)
+    B, k = 130, 7
+    W, h = head_of(elmo, rng.normal(0, 0.02, (L, d)), grid)
+    x = rng.normal(0, 1, (B, d))
+    x[5:], x[129] = 0, x[0]
+    X = bf16(x)
+    rowptr = np.concatenate([np.arange(6), np.full(B - 5, 5)]).astype(np.int32)
+    cols = rng.integers(0, L, 5).astype(np.int32)
+    got = run(elmo, h, X, rowptr, cols, k)
+    keep = [0, 1, 4, 5, 77, 129]
+    xs, w = X.double().cpu().numpy()[keep], W.double().cpu().numpy()
+    ptr = np.array([0, 1, 2, 3, 3, 3, 3], np.int32)
+    check([got[0][[0, 1, 4]], *(g[keep] for g in got[1:])], xs, w, grid, ptr, cols[[0, 1, 4]], k)
+    assert (got[3][5:129] == np.arange(k)).all()
+    h.close()
+
+
+@pytest.mark.parametrize("grid", ["bf16", "e4m3"])
+def test_scores_of_any_size(grid):
+    """Scores of 1e30 and more, all of one sign: nothing but them counts, however few labels the last tile has."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(3)
+    for L in (65, 5000):
+        w = np.abs(rng.normal(0, 0.02, (L, 128))) + 0.02
+        W, h = head_of(elmo, w, grid)
+        X = bf16(np.array([[-1.0], [1.0]]) * (np.abs(rng.normal(0, 1, (2, 128))) + 0.5) * 2.0**110)
+        rowptr, cols = np.array([0, 1, 2], np.int32), np.array([3, L - 1], np.int32)
+        logp, lse, H, idx, top = run(elmo, h, X, rowptr, cols, 3)
+        z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+        assert np.array_equal(idx, np.argsort(-z, 1, kind="stable")[:, :3])
+        assert np.abs(lse / z.max(1) - 1).max() < 1e-5 and (H == 0).all()
+        assert np.array_equal(top[:, 0] == 0, [True, True]) or np.abs(top[:, 0] / z.max(1)).max() < 1e-5
+        h.close()
+
+
 @pytest.mark.parametrize("kind", ["zeros", "few values", "best repeated", "two apart"])
 @pytest.mark.parametrize("grid,d", [("e4m3", 128), ("bf16", 832)])
 def test_ties_go_to_the_lower_label(grid, d, kind):
