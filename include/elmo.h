@@ -463,8 +463,8 @@ elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_
  *   Z[b, l] = sum_g s[l, g] sum_{j in group g} x[b, j] (u[l, j] - 8),
  * each group's sum and the sum over the groups in fp32.  The queries enter
  * with their bf16 values scaled by a power of two each (undone in fp32);
- * values below 2^-32 of their query's largest magnitude are rounded, to within
- * 2^-40 of that magnitude.  Any 4-bit copy in the stated layout may be given.
+ * values below 2^-31 of their query's largest magnitude are rounded, to within
+ * 2^-39 of that magnitude.  Any 4-bit copy in the stated layout may be given.
  *
  *   codes_dev, scales_dev, L, d, group : as in elmo_q4_pack.
  *   X_dev : bf16 [B x d], 1 <= B <= ELMO_MAX_PREDICT_BATCH.  Batches are taken
@@ -555,7 +555,8 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
  * labels of the head, X as its bf16 values.  The log-sum-exp and the entropy
  * are formed from tensor-core scores (fp32 accumulation; in 8-bit heads X
  * enters as a sum of two 8-bit numbers, which holds every bf16 value above
- * about 2^-15 of its query's largest magnitude exactly); the scores of the
+ * 2^-13 of its query's largest magnitude exactly and the others to within
+ * 2^-21 of it); the scores of the
  * given and of the listed labels are exact products summed in 64 bits, and the
  * k best labels are those of these exact scores, ties to the lower label.
  * (elmo_topk_predict ranks by an fp32 chain: the two lists may differ where

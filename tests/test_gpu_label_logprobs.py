@@ -41,13 +41,13 @@ def run(elmo, h, X, rowptr, cols, k, stream=None):
 
 def slack(x, w, p, d, grid):
     """How far lse and entropy of a query may be off: its tensor-core scores (2^-22 of the magnitudes summed an
-    instruction; in 8-bit heads also what two 8-bit numbers leave of x, at most 2^-23 of the query's largest magnitude
-    an element), then the fp32 sums: a term's 2.5 |d| E and 2^-22, chains of 8 and 2 additions, two per tile of a range
+    instruction; in 8-bit heads also what two 8-bit numbers leave of x, 2^-14 of at least 224 after scaling, so at most
+    2^-21 of the query's largest magnitude an element), then the fp32 sums: a term's 2.5 |d| E and 2^-22, chains of 8 and 2 additions, two per tile of a range
     (each may rescale), the ranges joined in 64 bits."""
     fp8 = grid != "bf16"
     steps = (2 if fp8 else 1) * -(-x.size * (1 if fp8 else 2) // 128) * 4
     mag = np.abs(w) @ np.abs(x)
-    dz = (steps * 2.0**-22 * mag + (2.0**-23 * np.abs(x).max() * np.abs(w).sum(1) if fp8 else 0)).max()
+    dz = (steps * 2.0**-22 * mag + (2.0**-21 * np.abs(x).max() * np.abs(w).sum(1) if fp8 else 0)).max()
     nt = 2 * (-(-w.shape[0] // 64) // 100 + 2)               # at least 100 ranges where there are as many tiles
     D, D2, R = -(p * d).sum(), (p * d * d).sum(), min(200.0, -d.min())
     chain = 2.0**-22 * (2 + nt) + (12 + 2 * nt) * E + 5 * R * E

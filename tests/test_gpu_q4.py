@@ -164,8 +164,8 @@ def test_scores_of_odd_queries():
     assert np.array_equal(got[4, rest & inf], z[4, rest & inf]) and np.isnan(got[4, rest & ~inf]).all()
     assert np.isnan(got[5]).all()
     for b in (0, 1, 2, 3, 6, 7):
-        # numbers below 2^-32 of the largest are rounded to within 2^-40 of it
-        coarse = 2.0**-40 * np.abs(x[b]).max() * np.abs((u.astype(np.float64) - 8) * np.repeat(s, group, 1)).sum(1)
+        # fp16 at a largest magnitude of 2^14 at least: a step of 2^-24, half of it 2^-39 of the largest
+        coarse = 2.0**-39 * np.abs(x[b]).max() * np.abs((u.astype(np.float64) - 8) * np.repeat(s, group, 1)).sum(1)
         bound = tolerance(d, group) * mag[b] + np.abs(z[b]) * 2.0**-24 + coarse + 2.0**-149
         assert (np.abs(got[b] - z[b]) <= bound)[rest].all(), b
 
