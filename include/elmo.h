@@ -501,6 +501,7 @@ typedef enum {
  *   rowptr_dev : int32 [B + 1], cols_dev int32 [nnz]: the given labels of each
  *                row (CSR), in any order, a label possibly more than once.
  *                Entries outside [0, nnz) are not read.
+ *   nnz        : 0 <= nnz <= 2^30 (ELMO_EUNSUPPORTED beyond).
  *   k          : 0 <= k <= min(L, ELMO_MAX_TOPK) labels listed.
  *   logp_dev   : fp32 [nnz], written: log p of each given label; NaN where
  *                the label id is outside [0, L).

@@ -21,7 +21,7 @@
 //      notes the maximum of every block of labels, which the running maximum
 //      needs anyway: keeping the best scores in the pass (a heap a query,
 //      limits shared between the ranges) took 1841 us for 3M labels and 256
-//      queries, where the pass now takes 880.
+//      queries, where the pass now takes 1032 in a loop.
 //   3. join: the ranges' sums in 64 bits; the given labels' scores recomputed
 //      exactly (products exact, sums in 64 bits); and the k best labels.  Let
 //      low be at most the k-th best block maximum.  k labels score at least
@@ -34,7 +34,9 @@
 //      a few times k, most labels would be scored again (1571 labels, 180
 //      queries, 5 best: 86 us).
 //   4. queries with too many labels within 2 delta (ties), or a head that is
-//      not finite, rank all labels by exact scores on the CUDA cores.
+//      not finite, rank all labels by exact scores on the CUDA cores: with all
+//      labels tied 1.8 ms for 500K bf16 labels x 768 and 1 to 4 queries, 38 ms
+//      for 3M E4M3 labels and 16.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
 // r1 the sum of what hi and lo leave, gamma = nsteps 2^-22: each of the nsteps
@@ -43,11 +45,11 @@
 // read off the tiles in shared memory by two spare warps.
 //
 // Bounds and times on B200.  Few queries: the read of W; 500K bf16 labels x
-// 768, 4 queries: pass 123 us (6.2 TB/s), all of it 152.  Many: the tensor
-// pipe, and with 64 labels an instruction the shared memory that both the
-// copies and the MMAs use; 3M E4M3 labels, 256 queries: pass 880 us at
-// 2.7 PFLOP/s of 8-bit products (two a weight), join 30, near 20, rank 12;
-// 1.11 to 1.17 ms in a loop, where the power limit lowers the clock.  Narrow
+// 768, 4 queries: pass 126 us (6.1 TB/s), all of it 158.  Many: the MMAs, most
+// likely by the shared memory that they and the copies use with 64 labels an
+// instruction (tensor pipe 62 % busy, 500K labels); 3M E4M3 labels, 256 queries:
+// pass 1032 us, 2.3 PFLOP/s of 8-bit products (two a weight), all of it 1174 in
+// a loop, at the power limit and 1440 MHz; 1028 for single calls.  Narrow
 // heads: the epilogue; 1M labels x 64, 128 queries: 70 us.
 #include <cuda.h>
 #include <float.h>
@@ -223,10 +225,9 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
 }
 
 // Four MMAs along K, 32 bytes each (D += A B, the first D = A B unless `more`),
-// A in tensor memory or in shared memory.  One thread issues them all, each of
-// its instructions waiting for the one before, so that an MMA of 64 labels,
-// 32 clocks of the tensor pipe, went out every 60 while its descriptor was
-// formed anew: here only the addresses move on.
+// A in tensor memory or in shared memory.  One thread issues them all; only the
+// addresses move on between them, which is a little faster than a descriptor
+// formed anew for each (300K labels x 1024: 276 to 268 us; x 768 unchanged).
 #define ELMO_MMA4(KIND, A_OPERAND)                                                          \
   "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("%1") ", %2, %3, p;\n\t"       \
   "tcgen05.mma.cta_group::1.kind::" KIND " [%0], " A_OPERAND("a1") ", b1, %3, q;\n\t"       \

@@ -20,8 +20,8 @@
 // On B200: 256 rows of 500K bf16 scores, pass 54 us (4.7 TB/s; the issue slots
 // bind: five and more instructions a score, one an exponential) and answers
 // 14 us behind it; one row of 3M fp32 scores 16 us in all, of which the pass is
-// 7; 33 rows of 4099 in one launch 13 us.  Gradient of the 256 rows: 86 us
-// (6.0 TB/s).
+// 7; 33 rows of 4099 in one launch 14 us.  Gradient of the 256 rows: 88 us
+// (5.8 TB/s).
 #include <cuda_bf16.h>
 
 #include "elmo_common.cuh"

@@ -228,9 +228,10 @@ cudaError_t run_pack(const void* W, int64_t n8, int32_t group, uint32_t* codes, 
 // 11; numbers below 2^-31 of the query's largest are rounded, to within 2^-39
 // of it, which is far below the fp32 sums' own rounding.
 //
-// Bound by the read of the codes: on B200, 3M labels x 768 in groups of 64 and
-// one query take 240 us (1.24 GB, 5.1 TB/s); the same ring with the arithmetic
-// left out takes 203 us.  500K labels, groups of 128, seven queries: 46 us.
+// Bound by the read of the codes and the unpacking together (1M labels: DRAM
+// 56 %, issue slots 60 %): on B200, 3M labels x 768 in groups of 64 and one query
+// take 260 us in a loop (1.24 GB, 4.8 TB/s); the same ring with the arithmetic
+// left out takes 203 us.  500K labels, groups of 128, seven queries: 48 us.
 // Eight warps of labels in place of sixteen took 307 us against 237; 24 warps,
 // larger requests and whole rows a stage changed nothing.
 constexpr int kQKB = 128;                 // bytes of a box's row: 256 codes
