@@ -136,7 +136,12 @@ elmo_status ensure_lp(HeadImpl* h, size_t bytes) {
     cudaGetLastError();
     return fail(ELMO_ENOMEM, "cannot allocate %zu bytes of log-probability workspace", want);
   }
-  if (h->lp) h->lp_old.push_back(h->lp);
+  try {
+    if (h->lp) h->lp_old.push_back(h->lp);
+  } catch (...) {                                          // no exception leaves a C entry
+    cudaFree(p);
+    return fail(ELMO_ENOMEM, "host allocation failed");
+  }
   h->lp = p;
   h->lp_bytes = want;
   h->lp_held += want;
