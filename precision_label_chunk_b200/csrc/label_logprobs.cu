@@ -35,7 +35,7 @@
 //      queries, 5 best: 86 us).
 //   4. queries with too many labels within 2 delta (ties), or a head that is
 //      not finite, rank all labels by exact scores on the CUDA cores: with all
-//      labels tied 1.8 ms for 500K bf16 labels x 768 and 1 to 4 queries, 38 ms
+//      labels tied 0.8 ms for 500K bf16 labels x 768 and 1 to 4 queries, 29 ms
 //      for 3M E4M3 labels and 16.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
@@ -85,6 +85,7 @@ constexpr int kNearAt = 8;                // labels that a warp scores at a time
 constexpr int kSegs = 74;                 // label segments of the exact path
 constexpr int kExactThreads = 256;
 constexpr int kExactChunk = 2048;
+constexpr int kExactLabels = 4;         // labels of a warp at a time
 
 // Doubles as whole numbers of the same order;
 // 0 for scores that are never listed (-inf, NaN); -0 and 0 are the same score
@@ -603,6 +604,33 @@ __device__ __forceinline__ double exact_score(const float* xs, const void* W, in
   return acc;
 }
 
+// The same for kM labels from l on, whose loads are in flight together; each sum
+// in exact_score's order.  Labels beyond `end` are read as `end`.
+template <int kFormat, int kM>
+__device__ __forceinline__ void exact_scores(const float* xs, const void* W, int64_t l, int64_t end, int d, int lane,
+                                             double (&acc)[kM]) {
+#pragma unroll
+  for (int m = 0; m < kM; ++m) acc[m] = 0.0;
+  for (int c = lane; c < d / 8; c += 32) {
+    Raw8<kFormat> r[kM];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) r[m] = load8<kFormat>(W, min(l + m, end), d, c);
+    double x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (double)xs[8 * c + e];
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      float f[8];
+      values8<kFormat>(r[m], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[m] = fma(x[e], (double)f[e], acc[m]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
+}
+
 // The same in fp32 for kM labels at a time.
 template <int kFormat, int kM>
 __device__ __forceinline__ void near_scores(const uint16_t* X, const void* W, const int64_t (&l)[kM], int d, int lane,
@@ -1036,12 +1064,19 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
     __syncthreads();
     for (int64_t a = l0; a < l1; a += kExactChunk) {
       const int n = (int)min((int64_t)kExactChunk, l1 - a);
-      for (int i = warp; i < n; i += kExactThreads / 32) {
-        const double z = exact_score<kFormat>(xs, A.W, a + i, A.d, lane);
-        if (lane == 0) key[i] = ord64(z);
+      for (int i = warp * kExactLabels; i < n; i += kExactThreads / 32 * kExactLabels) {
+        double z[kExactLabels];
+        exact_scores<kFormat, kExactLabels>(xs, A.W, a + i, l1 - 1, A.d, lane, z);
+#pragma unroll
+        for (int m = 0; m < kExactLabels; ++m)
+          if (lane == m && i + m < n) key[i + m] = ord64(z[m]);
       }
       if (tid < A.k) { key[kExactChunk + tid] = lk[tid]; old[tid] = li[tid]; }
       __syncthreads();
+      int enters = 0;                                  // of labels that all tie only the first chunk's do
+      for (int i = tid; i < n; i += kExactThreads)
+        enters |= key[i] != 0 && ranks_before(key[i], (int32_t)(a + i), lk[A.k - 1], li[A.k - 1]);
+      if (!__syncthreads_or(enters)) continue;
       auto at = [&](int i, uint64_t& k, int32_t& l) {
         if (i < n) { k = key[i]; l = (int32_t)(a + i); }
         else { k = key[kExactChunk + i - n]; l = old[i - n]; }
