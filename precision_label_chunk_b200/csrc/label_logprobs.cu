@@ -35,8 +35,8 @@
 //      queries, 5 best: 86 us).
 //   4. queries with too many labels within 2 delta (ties), or a head that is
 //      not finite, rank all labels by exact scores on the CUDA cores: with all
-//      labels tied 0.8 ms for 500K bf16 labels x 768 and 1 to 4 queries, 29 ms
-//      for 3M E4M3 labels and 16.
+//      labels tied 0.35 ms for 500K bf16 labels x 768 and one query, 0.87 for 4;
+//      21 ms for 3M E4M3 labels and 16.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
 // r1 the sum of what hi and lo leave, gamma = nsteps 2^-22: each of the nsteps
@@ -82,7 +82,6 @@ constexpr int kMaxNear = 4096;            // of their labels the ones near the k
 constexpr int kMaxExact = 1024;           // and of those the ones ranked by exact scores
 constexpr int kNearThreads = 256;
 constexpr int kNearAt = 8;                // labels that a warp scores at a time
-constexpr int kSegs = 74;                 // label segments of the exact path
 constexpr int kExactThreads = 256;
 constexpr int kExactChunk = 2048;
 constexpr int kExactLabels = 4;         // labels of a warp at a time
@@ -105,7 +104,7 @@ struct Args {
   const uint8_t *xa, *xb;                 // 8-bit heads: hi and lo codes [B][d]
   const void* W;
   int64_t L, label_base, labels_total;
-  int32_t d, B, G, k, nnz, fmt;
+  int32_t d, B, G, k, nnz, fmt, segs;
   int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
   int32_t nblk, nblkp, pairs;             // blocks of a stream, with padding; half tiles of a block
   int32_t streams;                        // kStreams; 0 where every label's score is kept: nblkp is their pitch
@@ -121,7 +120,7 @@ struct Args {
   int32_t* near_l;
   float* from;                            // [B] the fp32 score from which a label is near
   Stat* part;                             // [B][kStreams G] reference and sums in powers of two (Soft2)
-  uint64_t* seg_key;                      // [B][kSegs][k]
+  uint64_t* seg_key;                      // [B][segs][k]
   int32_t* seg_i;
   const int32_t *rowptr, *cols;
   float *logp, *lse, *entropy, *top_logp;
@@ -611,6 +610,8 @@ __device__ __forceinline__ void exact_scores(const float* xs, const void* W, int
                                              double (&acc)[kM]) {
 #pragma unroll
   for (int m = 0; m < kM; ++m) acc[m] = 0.0;
+  // two steps: one spills at 64 registers (500K bf16 labels tied, 4 queries: 1350 us against 865)
+#pragma unroll 2
   for (int c = lane; c < d / 8; c += 32) {
     Raw8<kFormat> r[kM];
 #pragma unroll
@@ -1054,10 +1055,10 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   const int nf = A.counts->nfail;
-  for (int64_t item = blockIdx.x; item < (int64_t)nf * kSegs; item += gridDim.x) {
-    const int r = (int)(item / kSegs), seg = (int)(item % kSegs);
+  for (int64_t item = blockIdx.x; item < (int64_t)nf * A.segs; item += gridDim.x) {
+    const int r = (int)(item / A.segs), seg = (int)(item % A.segs);
     const int b = A.fail[r];
-    const int64_t l0 = A.L * seg / kSegs, l1 = A.L * (seg + 1) / kSegs;
+    const int64_t l0 = A.L * seg / A.segs, l1 = A.L * (seg + 1) / A.segs;
     __syncthreads();
     for (int j = tid; j < A.d; j += kExactThreads) xs[j] = bf16_to_f32(A.X[(size_t)b * A.d + j]);
     if (tid < A.k) { lk[tid] = 0; li[tid] = 0x7FFFFFFF; }
@@ -1097,15 +1098,15 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
       }
       __syncthreads();
     }
-    uint64_t* sk = A.seg_key + (size_t)r * kSegs * A.k;
-    int32_t* si = A.seg_i + (size_t)r * kSegs * A.k;
+    uint64_t* sk = A.seg_key + (size_t)r * A.segs * A.k;
+    int32_t* si = A.seg_i + (size_t)r * A.segs * A.k;
     if (tid < A.k) {
       __stcg(reinterpret_cast<unsigned long long*>(sk) + seg * A.k + tid, (unsigned long long)lk[tid]);
       __stcg(si + seg * A.k + tid, li[tid]);
     }
     __threadfence();
     __syncthreads();
-    if (tid == 0) last = atomicAdd(A.done + r, 1) == kSegs - 1;
+    if (tid == 0) last = atomicAdd(A.done + r, 1) == A.segs - 1;
     __syncthreads();
     if (!last) continue;
     __threadfence();
@@ -1119,7 +1120,7 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
     for (int q = 0; q < A.k; ++q) {
       uint64_t k = 0;
       int32_t l = 0;
-      if (pk != 0) best_after(kSegs * A.k, at, pk, pi, rk, ri, k, l);
+      if (pk != 0) best_after(A.segs * A.k, at, pk, pi, rk, ri, k, l);
       if (tid == 0) {
         A.top_idx[(size_t)b * A.k + q] = k ? (int32_t)(l + A.label_base) : -1;
         A.top_logp[(size_t)b * A.k + q] = k ? (float)(ord64_value(k) - m - logs) : -INFINITY;
@@ -1136,6 +1137,13 @@ struct Layout {
   size_t xa, xb, xinv, n1, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
       rowstat, total;
 };
+
+// Label segments of a query on the exact path, a CTA each: 74 fill the GPU from
+// four queries on (two CTAs an SM).  Fewer queries take four times as many where
+// the scan is long against the join of segs x k entries, k times over (all
+// labels tied, one query: 500K bf16 labels, 5 best 788 -> 347 us, but 64 best
+// 1169 -> 1506; 3M E4M3 labels, 64 best 8.0 -> 2.7 ms).
+int exact_segments(int64_t L, int32_t B, int32_t k) { return B < 4 && L >= (int64_t)k << 15 ? 296 : 74; }
 
 int tile_labels(const elmo_head* h) { return h->d <= 768 ? 64 : 128; }
 
@@ -1175,8 +1183,8 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   o.from = take(4 * lists);
   o.bmax = take(k > 0 ? 4 * (size_t)(o.streams ? o.streams : 1) * B * o.nblkp : 0);
   o.part = take(sizeof(Stat) * (size_t)B * kStreams * o.G);
-  o.sk = take(8 * (size_t)B * kSegs * k);
-  o.si = take(4 * (size_t)B * kSegs * k);
+  o.sk = take(8 * (size_t)B * exact_segments(h->L, B, k) * k);
+  o.si = take(4 * (size_t)B * exact_segments(h->L, B, k) * k);
   o.rowstat = take(16 * (size_t)B);
   o.total = off;
   return o;
@@ -1252,6 +1260,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.nnz = nnz;
   A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.streams = o.streams;
   A.fmt = w_format(h);
+  A.segs = exact_segments(h->L, B, k);
   const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
   A.gamma = (float)nsteps * 0x1p-22f;
   A.xinv = reinterpret_cast<float*>(ws + o.xinv);

@@ -187,6 +187,29 @@ def test_ties_go_to_the_lower_label(grid, d, kind):
     h.close()
 
 
+@pytest.mark.parametrize("grid", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("L,B,k", [(32767, 3, 1), (32768, 3, 1), (32771, 1, 1), (65537, 2, 2), (65537, 4, 2), (66000, 1, 2)])
+def test_all_labels_tied_but_one(grid, L, B, k):
+    """Every list comes from the exact path, with many label segments a query and with few: labels that all tie, and one
+    above them that lies in a segment's last place, in the head's, or is the lowest."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L + B)
+    d = 128
+    x = np.abs(rng.normal(0, 1, (B, d))) + 0.1
+    for above in (None, 0, L * 5 // 296 - 1, L - 1):
+        w = np.full((L, d), 0.5)
+        if above is not None:
+            w[above] = 0.5625                                   # one step of E4M3 above
+            if grid == "e5m2":
+                w[above] = 0.625
+        W, h = head_of(elmo, w, grid)
+        logp, lse, H, idx, top = run(elmo, h, bf16(x), np.zeros(B + 1, np.int32), np.zeros(0, np.int32), k)
+        want = ([] if above is None else [above]) + [i for i in range(k + 1) if i != above]
+        assert (idx == np.array(want[:k])).all(), (above, idx)
+        h.close()
+
+
 @pytest.mark.parametrize("d", [128, 832])
 def test_values_that_are_not_finite(d):
     need_gpu()
