@@ -39,9 +39,14 @@
 //      21 ms for 3M E4M3 labels and 16.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
-// r1 the sum of what hi and lo leave, gamma = nsteps 2^-22: each of the nsteps
-// accumulating instructions is allowed 2^-22 of the magnitudes summed (a
-// thirty-second of the fp32 sum's d terms and 5 joins are less).  max|W| is
+// r1 the sum of what hi and lo leave.  gamma = 2^-24 times the products that
+// the accumulating instructions add (16 each of 16-bit, 32 of 8-bit operands).
+// How these round is documented nowhere.  Measured on B200, an instruction
+// cuts each product at 2^-25 of the largest addend, the sum so far among them,
+// and the sum to fp32: crafted queries lost 2^-21.0 of the magnitudes summed an
+// instruction of 16 products and 2^-20.0 of 32, where gamma allows 2^-20 and
+// 2^-19 (2^-22 puts such labels in the wrong order).  A
+// thirty-second of the fp32 sum's d terms and 5 joins are less.  max|W| is
 // read off the tiles in shared memory by two spare warps.
 //
 // Bounds and times on B200.  Few queries: the read of W; 500K bf16 labels x
@@ -1262,7 +1267,7 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.fmt = w_format(h);
   A.segs = exact_segments(h->L, B, k);
   const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
-  A.gamma = (float)nsteps * 0x1p-22f;
+  A.gamma = (float)nsteps * (fp8 ? 32.0f : 16.0f) * 0x1p-24f;
   A.xinv = reinterpret_cast<float*>(ws + o.xinv);
   A.n1 = reinterpret_cast<float*>(ws + o.n1);
   A.r1 = reinterpret_cast<float*>(ws + o.r1);
