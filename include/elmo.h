@@ -493,7 +493,7 @@ typedef enum {
  * in 64 bits.  A score of -inf masks its label: its log p is -inf, and it is
  * never listed.  A row with every label masked has lse = -inf, H = 0 and
  * log p = -inf.  A row holding a NaN has NaN statistics; one holding +inf
- * has lse = +inf and H = NaN.
+ * and no NaN has lse = +inf and H = NaN.
  *
  *   Z_dev      : [B x L] scores of type zt, row b at element b * ldz
  *                (ldz >= L); any alignment of its elements.

@@ -434,9 +434,13 @@ __device__ __forceinline__ void finish_row(const Args& A, const T* z, int shift,
     logs = 0.0;
     lse = s == 0.0 ? -INFINITY : NAN;
     H = s == 0.0 ? 0.0 : NAN;
+  } else if (m == INFINITY) {                        // s counts the infinities, a NaN makes it NaN
+    logs = 0.0;
+    lse = isnan(s) ? (double)NAN : (double)INFINITY;
+    H = NAN;
   } else {
     logs = log(s);
-    lse = m == INFINITY ? (double)INFINITY : m + logs;
+    lse = m + logs;
     H = logs - t / s;
   }
   const int tid = threadIdx.x;

@@ -91,6 +91,7 @@ struct Soft {
       unpair(add2(pair(v[2 * c], v[2 * c + 1]), nm), a, b);
       return pair(max_nan(a, kSoftFloor), max_nan(b, kSoftFloor));
     }, ss, tt);
+    if (tt != tt) slow32(v, m0, ss, tt);
     s += ss;
     t += tt;
   }
@@ -114,11 +115,12 @@ struct Soft {
     ss = s0 + s1;
     tt = t0 + t1;
   }
+  // one by one: scores of +inf count 1 each beside a maximum of +inf, so that only a NaN makes the sums NaN
   __device__ __forceinline__ void slow32(const float (&v)[32], float m0, float& ss, float& tt) const {
     ss = tt = 0.0f;
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      const float d = max_nan(v[c] - m0, kSoftFloor), e = ex2(d * kLog2e);
+      const float d = v[c] == m0 ? 0.0f : max_nan(v[c] - m0, kSoftFloor), e = ex2(d * kLog2e);
       ss += e;
       tt = fmaf(e, d, tt);
     }

@@ -14,6 +14,45 @@ pytestmark = pytest.mark.gpu
 INF, NAN = np.inf, np.nan
 
 
+# ---------------------------------------------------------------- rows of scores
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("L", [3, 100, 5000, 40_000, 400_000])
+def test_rows_with_nan_beside_infinity(dtype, L):
+    """A NaN spoils a row whatever else it holds, in the same vector, block or part as an infinity or far from it; rows
+    with infinities alone keep lse = +inf."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L)
+    places = [(0, 1), (1, 0), (0, L - 1), (L - 1, 0), (L // 2, L // 2 + 1), (L // 3, 2 * L // 3)]
+    z = rng.normal(0, 3, (len(places) + 4, L)).astype(np.float32)
+    for b, (n, i) in enumerate(places):
+        z[b, i], z[b, n] = INF, NAN
+    n = len(places)
+    z[n, 0], z[n, 2] = INF, INF                                 # two infinities and no NaN
+    z[n + 1, 1] = INF
+    z[n + 2] = np.where(np.arange(L) == 1, NAN, -INF)
+    z[n + 3] = np.where(np.arange(L) == 1, INF, -INF)
+    rowptr = np.arange(len(z) + 1, dtype=np.int32)
+    cols = np.full(len(z), 2, np.int32)
+    cols[3] = cols[2] = 1
+    Z = score_ops.on_gpu(z, dtype)
+    logp, lse, H, idx, top = score_ops.scored(elmo, Z, rowptr, cols, 2)
+    spoiled = np.r_[0:n, n + 2]
+    assert np.isnan(lse[spoiled]).all() and np.isnan(H).all()
+    assert np.isnan(logp[spoiled]).all()
+    assert (lse[[n, n + 1, n + 3]] == INF).all()
+    assert np.isnan(logp[n]) and logp[n + 1] == -INF and logp[n + 3] == -INF
+    best = np.where(np.isnan(z), -INF, z)
+    first = np.argmax(best, 1)
+    assert (idx[:, 0] == np.where(best.max(1) > -INF, first, -1)).all()
+    # the gradient of a spoiled row is NaN, that of a row whose lse is infinite zero
+    dZ = torch.empty_like(Z)
+    up = lambda a: torch.from_numpy(a).cuda()   # noqa: E731
+    elmo.elmo_score_logprobs_backward(Z, up(rowptr), up(cols), up(lse), None, torch.ones(len(z), device="cuda"), None, None, dZ)
+    dz = dZ.float().cpu().numpy()
+    assert np.isnan(dz[spoiled]).all() and (dz[[n, n + 1, n + 3]] == 0).all()
+
+
 # ---------------------------------------------------------------- heads
 @pytest.mark.parametrize("grid,L,d", [("bf16", 3000, 768), ("bf16", 20_000, 512), ("bf16", 3000, 1024), ("e4m3", 3000, 768),
                                       ("e4m3", 20_000, 768), ("e5m2", 3000, 1024)])
