@@ -840,8 +840,9 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
         H = s == 0.0 ? 0.0 : NAN;
         m = lse;
         logs = 0.0;
-      } else if (mf == INFINITY) {
-        lse = m;
+      } else if (mf == INFINITY) {                     // s counts the infinities, a NaN makes it NaN
+        lse = m = isnan(s) ? NAN : m;
+        H = NAN;
         logs = 0.0;
       }
       if (bad) lse = H = m = NAN;

@@ -189,7 +189,9 @@ struct Soft2 {
       const float m0 = m > -INFINITY ? m : 0.0f;
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        const float d = max_nan(far ? (v[c] - m0) * c2 : fmaf(v[c], c2, -r), -300.0f), e = ex2(d);
+        // scores of +inf count 1 each beside a maximum of +inf, as in Soft
+        const float d = far && v[c] == m0 ? 0.0f : max_nan(far ? (v[c] - m0) * c2 : fmaf(v[c], c2, -r), -300.0f);
+        const float e = ex2(d);
         ss += e;
         tt = fmaf(e, d, tt);
       }

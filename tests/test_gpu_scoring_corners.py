@@ -54,6 +54,28 @@ def test_rows_with_nan_beside_infinity(dtype, L):
 
 
 # ---------------------------------------------------------------- heads
+@pytest.mark.parametrize("grid,d", [("bf16", 128), ("bf16", 832), ("e5m2", 128), ("e5m2", 832)])
+@pytest.mark.parametrize("L", [2000, 60_000])
+def test_weights_of_nan_beside_infinity(grid, d, L):
+    """A NaN score spoils the statistics beside an infinite one too; the list goes by the scores that are numbers."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L + d)
+    w = rng.normal(0, 0.02, (L, d))
+    x = np.abs(rng.normal(0, 1, (3, d))) + 0.1
+    rowptr, cols = np.array([0, 2, 4, 6], np.int32), np.array([7, 1, 7, 2, 7, 3], np.int32)
+    for infinite, spoiled in ((7, 9), (9, 7), (7, L - 1), (L - 1, 7)):
+        ww = w.copy()
+        ww[infinite, 3], ww[spoiled, 0] = INF, NAN
+        W, h = head_ops.head_of(elmo, ww, grid)
+        logp, lse, H, idx, top = head_ops.run(elmo, h, head_ops.bf16(x), rowptr, cols, 3)
+        assert np.isnan(lse).all() and np.isnan(H).all() and np.isnan(logp).all()
+        z = head_ops.bf16(x).double().cpu().numpy() @ np.where(np.isnan(ww), 0, W.double().cpu().numpy()).T
+        z[:, spoiled] = -INF
+        assert np.array_equal(idx, np.argsort(-z, 1, kind="stable")[:, :3]) and (idx[:, 0] == infinite).all()
+        h.close()
+
+
 @pytest.mark.parametrize("grid,L,d", [("bf16", 3000, 768), ("bf16", 20_000, 512), ("bf16", 3000, 1024), ("e4m3", 3000, 768),
                                       ("e4m3", 20_000, 768), ("e5m2", 3000, 1024)])
 def test_products_that_the_tensor_cores_cut_off(grid, L, d):
