@@ -269,6 +269,27 @@ __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint
 #undef ELMO_A_TMEM
 #undef ELMO_A_SMEM
 
+// The score of a label with a weight that is not finite, from its products with
+// such weights alone: an infinity, or NaN.  In an E5M2 head the tensor cores'
+// is no use: hi w + lo w of an infinite w is NaN wherever lo is zero or of the
+// other sign.
+__device__ __noinline__ float infinite_score(const uint16_t* x, const uint8_t* w, int d) {
+  float z = 0.0f;
+  for (int j = 0; j < d && z == z; j += 16) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + j));
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((((u[i] & 0x7F7F7F7Fu) + 0x04040404u) & 0x80808080u) == 0) continue;    // magnitudes below 0x7C: all finite
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t c = (u[i] >> (8 * e)) & 0xFFu;
+        if ((c & 0x7Fu) >= 0x7Cu) z += bf16_to_f32(x[j + 4 * i + e]) * e5m2_to_f32((uint8_t)c);
+      }
+    }
+  }
+  return z == 0.0f ? NAN : z;
+}
+
 // kFp8: 8-bit head (kW5: E5M2 weights).  kXs = 0: d <= 768, X (two 8-bit or
 // one bf16 operand, 2 d bytes a query) stays in the first TMEM columns, d / 2
 // of the 512, and tiles are 64 labels; kXs = 1: wider heads, X comes through
@@ -432,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, r = quad * 32 + lane, row = p * 128 + r;
     const bool live = row < A.B;
     const float inv = live ? A.xinv[row] : 1.0f;       // scores are inv times the accumulators
+    const bool finite = kW5 && live && A.rflag[row] == 0;
     Soft2 soft(inv);
     const bool keep = A.k > 0 && A.streams == 0, lists = A.k > 0 && !keep && live;
     float* bm = A.bmax + (keep ? (size_t)row : (size_t)row * kStreams + stream) * A.nblkp;
@@ -474,7 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float mx = max32(v);
           best = fmaxf(best, mx);
-          soft.add32(v, mx);
+          soft.add32(v, mx, [&](float (&bad)[32]) {
+            if (!kW5 || !finite) return false;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (bad[c] != bad[c])
+                bad[c] = infinite_score(A.X + (size_t)row * A.d, static_cast<const uint8_t*>(A.W) + (size_t)(l0 + c) * A.d, A.d);
+            return true;
+          });
           if (keep) {
 #pragma unroll
             for (int c = 0; c < 32; c += 4)

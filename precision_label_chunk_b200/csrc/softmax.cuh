@@ -157,17 +157,22 @@ struct Soft2 {
 
   __device__ __forceinline__ explicit Soft2(float inv) : c2(inv * kLog2e) {}
 
-  __device__ __forceinline__ void add32(const float (&v)[32], float mx) {
-    if (mx > m) {
-      const float to = mx * c2;
-      if (m > -INFINITY) {
-        const float d = fmaxf(fabsf(to) > kFar || fabsf(r) > kFar ? (m - mx) * c2 : r - to, -300.0f), c = ex2(d);
-        t = c * fmaf(s, d, t);
-        s *= c;
-      }
-      m = mx;
-      r = to;
+  __device__ __forceinline__ void raise(float mx) {    // m <- mx, mx > m
+    const float to = mx * c2;
+    if (m > -INFINITY) {
+      const float d = fmaxf(fabsf(to) > kFar || fabsf(r) > kFar ? (m - mx) * c2 : r - to, -300.0f), c = ex2(d);
+      t = c * fmaf(s, d, t);
+      s *= c;
     }
+    m = mx;
+    r = to;
+  }
+
+  // 32 accumulators with the maximum mx.  Where one of them is NaN, repair(v) may
+  // put others in their place, and says whether it did.
+  template <typename F>
+  __device__ __forceinline__ void add32(float (&v)[32], float mx, F repair) {
+    if (mx > m) raise(mx);
     const f2 cc = pair(c2, c2), nr = pair(-r, -r);
     f2 ps[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)}, pt[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
@@ -183,8 +188,12 @@ struct Soft2 {
     unpair(add2(ps[0], ps[1]), s0, s1);
     unpair(add2(pt[0], pt[1]), t0, t1);
     float ss = s0 + s1, tt = t0 + t1;
-    const bool far = fabsf(r) > kFar;
-    if (tt != tt || far) {                             // also a score of -inf (0 times infinity), or a NaN
+    if (tt != tt || fabsf(r) > kFar) {                 // also a score of -inf (0 times infinity), or a NaN
+      if (tt != tt && repair(v)) {
+        const float to = max32(v);
+        if (to > m) raise(to);
+      }
+      const bool far = fabsf(r) > kFar;
       ss = tt = 0.0f;
       const float m0 = m > -INFINITY ? m : 0.0f;
 #pragma unroll

@@ -76,6 +76,44 @@ def test_weights_of_nan_beside_infinity(grid, d, L):
         h.close()
 
 
+@pytest.mark.parametrize("d", [128, 832])
+@pytest.mark.parametrize("L,k", [(2000, 3), (2000, 0), (20_000, 3)])
+def test_infinite_weights_of_an_e5m2_head(d, L, k):
+    """An infinite weight makes an infinite score, whatever the two 8-bit numbers that a query's element becomes are."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L + d)
+    w = rng.normal(0, 0.02, (L, d))
+    B = 6
+    x = rng.normal(0, 1, (B, d))
+    x[:, 5] = [1.0, 1.0078125, 1.0703125, -1.0, -1.0703125, 0.0]  # the second number zero, of the same and of the other sign
+    rowptr, cols = np.arange(0, 2 * B + 1, 2).astype(np.int32), np.tile(np.array([7, 1], np.int32), B)
+    X = head_ops.bf16(x)
+    for value in (INF, -INF):
+        ww = w.copy()
+        ww[7, 5] = value
+        W, h = head_ops.head_of(elmo, ww, "e5m2")
+        logp, lse, H, idx, top = head_ops.run(elmo, h, X, rowptr, cols, k)
+        with np.errstate(invalid="ignore"):
+            z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+        assert np.isnan(lse[5]) and np.isnan(H[5]) and np.isnan(logp[10:]).all()      # 0 times infinity
+        for b in range(5):
+            if z[b, 7] == INF:
+                assert lse[b] == INF and np.isnan(H[b]) and np.isnan(logp[2 * b]) and logp[2 * b + 1] == -INF
+            else:
+                assert z[b, 7] == -INF
+                rest = np.delete(z[b], 7)
+                m = rest.max()
+                want = m + np.log(np.exp(rest - m).sum())
+                p = np.exp(rest - want)
+                assert abs(lse[b] - want) < 1e-4 and abs(H[b] + (p * (rest - want)).sum()) < 1e-3
+                assert logp[2 * b] == -INF and abs(logp[2 * b + 1] - (z[b, 1] - want)) < 1e-4
+        if k:
+            order = np.argsort(-np.where(np.isnan(z), -INF, z), 1, kind="stable")[:, :k]
+            assert np.array_equal(idx, order)
+        h.close()
+
+
 @pytest.mark.parametrize("grid,L,d", [("bf16", 3000, 768), ("bf16", 20_000, 512), ("bf16", 3000, 1024), ("e4m3", 3000, 768),
                                       ("e4m3", 20_000, 768), ("e5m2", 3000, 1024)])
 def test_products_that_the_tensor_cores_cut_off(grid, L, d):
