@@ -570,9 +570,12 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
  *   top_idx_dev, top_logp_dev : as in elmo_score_logprobs; a given label
  *                outside [0, L) also sets ELMO_EDATA in the status word.
  * Weights that are not finite count as the scores that they make (see
- * elmo_score_logprobs).  Queries whose list the tensor-core scores cannot
- * settle (ties, weights that are not finite) are ranked over all labels on the
- * CUDA cores, which takes far longer.  ELMO_EUNSUPPORTED on a head made by
+ * elmo_score_logprobs).  Scores of 2^127 and more, and sums that leave fp32's
+ * range on the way to a score, make the log-sum-exp and the entropy infinite
+ * or NaN; the list holds all the same.  Queries whose list the tensor-core
+ * scores cannot settle (ties, sums that may leave fp32's range, weights that
+ * are not finite) are ranked over all labels on the CUDA cores, which takes far
+ * longer.  ELMO_EUNSUPPORTED on a head made by
  * elmo_init_head_shard that does not hold all labels.
  * The workspace is the head's: the first call of a size allocates (call once
  * before capturing into a CUDA graph); calls on one head must not overlap on

@@ -33,10 +33,11 @@
 //      their tensor-core scores in place of the maxima: with fewer blocks than
 //      a few times k, most labels would be scored again (1571 labels, 180
 //      queries, 5 best: 86 us).
-//   4. queries with too many labels within 2 delta (ties), or a head that is
-//      not finite, rank all labels by exact scores on the CUDA cores: with all
-//      labels tied 0.35 ms for 500K bf16 labels x 768 and one query, 0.87 for 4;
-//      21 ms for 3M E4M3 labels and 16.
+//   4. queries with too many labels within 2 delta (ties), or with sums that
+//      may leave fp32's range, or a head that is not finite, rank all labels
+//      by exact scores on the CUDA cores: with all labels tied 0.35 ms for 500K
+//      bf16 labels x 768 and one query, 0.87 for 4; 21 ms for 3M E4M3 labels
+//      and 16.
 //
 // delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
 // r1 the sum of what hi and lo leave.  gamma = 2^-24 times the products that
@@ -730,10 +731,13 @@ __device__ __forceinline__ float lower_bound_kth(SmemB* S, float best, int k) {
   return S->low;
 }
 
-// 2 delta of a query, rounded up; 2^-126 for subnormal partial sums
+// 2 delta of a query, rounded up; 2^-126 for subnormal partial sums.  Infinite
+// where the weights are not finite or a sum may leave fp32's range on its way
+// (to an infinity or a NaN that no bound holds for).
 __device__ __forceinline__ float two_delta(const Args& A, int b) {
-  float d = __fmul_ru(A.gamma, __fadd_ru(A.n1[b], A.r1[b]));
-  d = __fmul_ru(__fadd_ru(d, A.r1[b]), max_weight(A.counts->wmax, A.fmt));
+  const float n = __fadd_ru(A.n1[b], A.r1[b]), w = max_weight(A.counts->wmax, A.fmt);
+  if (!(__fmul_ru(n, w) < 0x1p126f)) return INFINITY;
+  const float d = __fmul_ru(__fadd_ru(__fmul_ru(A.gamma, n), A.r1[b]), w);
   return __fmul_ru(2.0f, __fadd_ru(d, 0x1p-126f));
 }
 
@@ -896,7 +900,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
         A.top_logp[(size_t)b * A.k + i] = bad ? -INFINITY : (float)(0.0 - m - logs);
       }
     } else {
-      bool ok = two < INFINITY;                        // not so for weights that are not finite
+      bool ok = two < INFINITY;                        // not so for weights that are not finite, or sums that overflow
       // n maxima, -inf in the padding between streams; or all the labels' scores
       const bool keep = A.streams == 0;
       const float* bm = A.bmax + (size_t)b * (keep ? 1 : kStreams) * A.nblkp;

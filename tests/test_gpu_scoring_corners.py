@@ -114,6 +114,26 @@ def test_infinite_weights_of_an_e5m2_head(d, L, k):
         h.close()
 
 
+@pytest.mark.parametrize("L", [3000, 20_000])
+def test_lists_where_sums_leave_the_range(L):
+    """Scores that are ordinary numbers, but whose fp32 sums pass through an infinity: the list is still that of the
+    exact scores."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L)
+    d, k = 128, 5
+    w = rng.normal(0, 1, (L, d)) * 2.0**88
+    for at, lift in ((77, 1.25), (L - 5, 1.125)):               # -2^129 half way, then 2^127 and 2^126 in all
+        w[at, :64], w[at, 64:] = -2.0**96, lift * 2.0**96
+    W, h = head_ops.head_of(elmo, w, "bf16")
+    X = head_ops.bf16(np.full((2, d), 2.0**27))
+    idx = head_ops.run(elmo, h, X, np.zeros(3, np.int32), np.zeros(0, np.int32), k)[3]
+    z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+    assert z.max() < 3e38
+    assert np.array_equal(idx, np.argsort(-z, 1, kind="stable")[:, :k]) and (idx[:, :2] == [77, L - 5]).all()
+    h.close()
+
+
 @pytest.mark.parametrize("grid,L,d", [("bf16", 3000, 768), ("bf16", 20_000, 512), ("bf16", 3000, 1024), ("e4m3", 3000, 768),
                                       ("e4m3", 20_000, 768), ("e5m2", 3000, 1024)])
 def test_products_that_the_tensor_cores_cut_off(grid, L, d):
