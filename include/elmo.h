@@ -464,7 +464,8 @@ elmo_status elmo_q4_unpack(const void* codes_dev, const void* scales_dev, int64_
  * each group's sum and the sum over the groups in fp32.  The queries enter
  * with their bf16 values scaled by a power of two each (undone in fp32);
  * values below 2^-31 of their query's largest magnitude are rounded, to within
- * 2^-39 of that magnitude.  Any 4-bit copy in the stated layout may be given.
+ * 2^-39 of that magnitude.  Where these sums leave fp32's range the score is
+ * formed in 64 bits instead.  Any 4-bit copy in the stated layout may be given.
  *
  *   codes_dev, scales_dev, L, d, group : as in elmo_q4_pack.
  *   X_dev : bf16 [B x d], 1 <= B <= ELMO_MAX_PREDICT_BATCH.  Batches are taken

@@ -227,6 +227,9 @@ cudaError_t run_pack(const void* W, int64_t n8, int32_t group, uint32_t* codes, 
 // its largest magnitude into [2^14, 2^15).  A bf16 number's 8 bits fit fp16's
 // 11; numbers below 2^-31 of the query's largest are rounded, to within 2^-39
 // of it, which is far below the fp32 sums' own rounding.
+// The scaling is undone last, so that under scales of 2^100 and more the sums may
+// overflow where the score does not: a score that is not finite, of a query that
+// is, is formed again in 64 bits.
 //
 // Bound by the read of the codes and the unpacking together (1M labels: DRAM
 // 56 %, issue slots 60 %): on B200, 3M labels x 768 in groups of 64 and one query
@@ -320,6 +323,7 @@ __device__ __forceinline__ void pow2_factors(int e, float& f0, float& f1) {
 struct SmemQ {
   uint64_t full[kQMaxStages], empty[kQMaxStages];
   int32_t exponent[8 * kQMaxNB];
+  int32_t finite[8 * kQMaxNB];
   int abort;
 };
 
@@ -333,6 +337,7 @@ size_t q4_fixed(int d, int group) {
 }
 
 struct Q4Args {
+  const uint8_t* codes;
   const uint16_t* scales;
   const uint16_t* X;
   float* Z;
@@ -340,12 +345,44 @@ struct Q4Args {
   int32_t d, B, stages;
 };
 
+// The scores that a thread has stored, label0 and those 8 apart from it, of
+// queries 8 nb + 2 t and the next: those that are not finite again in 64 bits,
+// where the query is.
+template <int kG>
+__device__ __noinline__ void q4_scores_again(const Q4Args& A, const int32_t* finite, int64_t label0, int labels, int b0,
+                                             int nbs, int t) {
+  for (int nb = 0; nb < nbs; ++nb) {
+    for (int c = 0; c < 2; ++c) {
+      const int n = nb * 8 + 2 * t + c;
+      if (b0 + n >= A.B || !finite[n]) continue;
+      for (int i = 0; i < labels; ++i) {
+        const int64_t l = label0 + 8 * i;
+        float* to = A.Z + (int64_t)(b0 + n) * A.ldz + l;
+        if (l >= A.L || fabsf(*to) < INFINITY) continue;
+        const uint8_t* codes = A.codes + l * (A.d / 2);
+        const uint16_t* scales = A.scales + l * (A.d / kG);
+        const uint16_t* x = A.X + (size_t)(b0 + n) * A.d;
+        double z = 0.0;
+        for (int g = 0; g < A.d / kG; ++g) {
+          double sum = 0.0;
+          for (int j = g * kG; j < (g + 1) * kG; j += 8) {
+            const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(codes + j / 2));
+            for (int e = 0; e < 8; ++e) sum += (double)bf16_to_f32(x[j + e]) * ((int)(u >> (4 * e) & 15u) - 8);
+          }
+          z += (double)bf16_to_f32(scales[g]) * sum;
+        }
+        *to = (float)z;
+      }
+    }
+  }
+}
+
 // kMT: 16-label blocks of a warp; kNB: 8-query blocks of this pass (grid.y
 // walks over the batch 8 kNB queries at a time); kWarps warps of labels and
 // one for the TMA.
 template <int kG, int kMT, int kNB, int kWarps>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
-    q4_scores_kernel(const __grid_constant__ CUtensorMap tmQ, const Q4Args A) {
+    q4_scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Q4Args A) {
   constexpr int kRows = 16 * kMT;                    // labels of a warp
   constexpr int kTile = kRows * kWarps;              // labels of a tile
   constexpr uint32_t kStage = kTile * kQKB;
@@ -390,7 +427,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
   // X into fragment order.  The exponents first: warp w takes queries w, w + kWarps, ...
   if (warp < kWarps) {
     for (int n = warp; n < 8 * kNB; n += kWarps) {
-      uint32_t m = 0;
+      uint32_t m = 0, most = 0;
       if (b0 + n < A.B) {
         const uint4* xr = reinterpret_cast<const uint4*>(A.X + (size_t)(b0 + n) * A.d);
         for (int j = lane; j < A.d / 8; j += 32) {
@@ -401,11 +438,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
             const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
             if (lo < 0x7F80u) m = max(m, lo);          // the largest finite magnitude
             if (hi < 0x7F80u) m = max(m, hi);
+            most = max(most, max(lo, hi));
           }
         }
         for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       }
-      if (lane == 0) S->exponent[n] = m == 0 ? 0 : 141 - max((int)(m >> 7), 1);
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
+      if (lane == 0) {
+        S->exponent[n] = m == 0 ? 0 : 141 - max((int)(m >> 7), 1);
+        S->finite[n] = most < 0x7F80u;
+      }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     const int nf = ng * kWords * kNB * 32;
@@ -462,6 +504,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
     const int row0 = warp * kRows + q4_row<kG>(g);     // of the tile: fragment rows g, g + 8 are rows row0, row0 + 8
     // byte t kG / 8 of a row's group j, swizzled; rows row0 + 8 i share row & 7
     const uint32_t mine = smem_u32(ring) + (uint32_t)row0 * kQKB, swz = (uint32_t)(row0 & 7) << 4;
+    float odd = 0.0f;                                  // NaN once a score is not finite
     for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x, buf ^= 1) {
       cp_async_wait();
       __syncwarp();
@@ -538,6 +581,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
           for (int r = lane; r < kRows; r += 32)
             for (int n = b0; n < min(b0 + 8 * kNB, A.B); ++n)
               if (tl * kTile + warp * kRows + r < A.L) A.Z[(int64_t)n * A.ldz + tl * kTile + warp * kRows + r] = NAN;
+        odd = 0.0f;
         break;
       }
 #pragma unroll
@@ -554,11 +598,19 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
           for (int m = 0; m < kMT; ++m) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              if (16 * m + 8 * h < left) __stcs(z + 16 * m + 8 * h, out[m][nb][2 * h + c] * f0 * f1);
+              if (16 * m + 8 * h < left) {
+                const float v = out[m][nb][2 * h + c] * f0 * f1;
+                __stcs(z + 16 * m + 8 * h, v);
+                odd = __fmaf_rn(v, 0.0f, odd);
+              }
           }
         }
       }
     }
+    // after the tiles: a call among them costs registers (500K labels, 32 queries: 107 us against 124)
+    if (odd != 0.0f)
+      for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x)
+        q4_scores_again<kG>(A, S->finite, tile * kTile + row0, 2 * kMT, b0, kNB, t);
   }
   __syncthreads();
   if (*abort) __nanosleep(20000);       // copies still in flight land before the shared memory is given up
@@ -627,7 +679,7 @@ cudaError_t launch_q4_unpack(const uint8_t* codes, const uint16_t* scales, int64
 
 cudaError_t launch_q4_scores(const uint8_t* codes, const uint16_t* scales, int64_t L, int32_t d, int32_t group,
                              const uint16_t* X, int32_t B, float* Z, int64_t ldz, cudaStream_t s) {
-  const Q4Args A{scales, X, Z, L, ldz, d, B, 0};
+  const Q4Args A{codes, scales, X, Z, L, ldz, d, B, 0};
   if (group == 32) return run_q4_group<32>(codes, A, s);
   if (group == 64) return run_q4_group<64>(codes, A, s);
   return run_q4_group<128>(codes, A, s);

@@ -161,3 +161,32 @@ def test_products_that_the_tensor_cores_cut_off(grid, L, d):
     one = head_ops.run(elmo, h, X, np.zeros(3, np.int32), np.zeros(0, np.int32), 1)[3]
     assert (idx == [a, b]).all() and (one == a).all()
     h.close()
+
+
+# ---------------------------------------------------------------- 4-bit copies
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("L,B", [(300, 1), (300, 9), (300, 30), (40_011, 2), (80_003, 8)])
+def test_scores_of_large_scales(group, L, B):
+    """Scales up to the largest that packing makes: scores that fp32 holds come out, and only the others are infinite."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(L + B + group)
+    d = 256
+    u = rng.integers(0, 16, (L, d)).astype(np.uint8)
+    s = q4_ops.bf16_of(rng.uniform(1, 2, (L, d // group)) * 2.0 ** rng.integers(85, 122, (L, 1)))
+    s[5:40] = q4_ops.bf16_of(np.abs(rng.normal(0, 0.01, (35, d // group))))   # ordinary labels among them
+    x = q4_ops.bf16_of(rng.normal(0, 1, (B, d)) * 2.0 ** rng.integers(-20, 2, (B, 1)))
+    Z = torch.full((B, L + 3), 123.0, device="cuda")
+    elmo.elmo_q4_scores(torch.from_numpy(q4_ops.nibbles(u)).cuda(), torch.from_numpy(s).to(torch.bfloat16).cuda(),
+                        torch.from_numpy(x).to(torch.bfloat16).cuda(), Z[:, :L])
+    z, mag = q4_ops.scored(u, s, x, group)
+    got = Z.double().cpu().numpy()
+    assert (got[:, L:] == 123.0).all()
+    got, most = got[:, :L], float(np.finfo(np.float32).max)
+    bound = q4_ops.tolerance(d, group) * mag + np.abs(z) * 2.0**-24
+    holds = np.abs(z) + bound < most
+    assert (np.abs(np.where(holds, got, 0) - np.where(holds, z, 0)) <= bound)[holds].all()
+    over = np.abs(z) - bound > most * (1 + 2.0**-24)
+    assert (got[over] == np.sign(z[over]) * INF).all()
+    scaled = np.abs(z) * 2.0 ** (14 - np.floor(np.log2(np.abs(x).max(1))))[:, None]
+    assert (scaled > most)[holds].mean() > 0.1                  # with each query's largest element in [2^14, 2^15)
