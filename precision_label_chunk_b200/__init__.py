@@ -359,10 +359,11 @@ def elmo_precision_at_k(idx: torch.Tensor, rowptr: torch.Tensor, cols: torch.Ten
 
 
 _BF16_BITS = (torch.bfloat16, torch.int16)
-_FP8_CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
+_E4M3_CODES = (torch.uint8, torch.float8_e4m3fn)
+_WEIGHTS = {BF16: _BF16_BITS, FP8_E4M3: _E4M3_CODES, FP8_E4M3_GE5M2: _E4M3_CODES, FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
 _SCORE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -382,7 +383,7 @@ def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales
     dt = _dt(dtype)
     L, d = W.shape
     group = int(group)
-    _check(load().elmo_q4_pack(_arg("W", W, (L, d), _BF16_BITS if dt == BF16 else _FP8_CODES), L, d, dt, group,
+    _check(load().elmo_q4_pack(_arg("W", W, (L, d), _WEIGHTS[dt]), L, d, dt, group,
                                _arg("codes", codes, (L, d // 2), _U8),
                                _arg("scales", scales, (L, d // group if group > 0 else 0), _BF16_BITS),
                                _stream(stream)))
