@@ -138,9 +138,15 @@ def _check(rc: int):
         raise ElmoError(rc, elmo_last_error())
 
 
+# The handle of a device's current stream without a Stream object around it, which takes 3.6 us to build where a small
+# call takes 10 in all.  torch promises no such function: where it is missing the public one answers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        device = torch.cuda.current_device()
+        return ctypes.c_void_p(_raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -158,19 +164,21 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _arg(name, t, shape, dtypes, pitch=False):
-    """The device address of an argument of the scoring calls, checked: its shape and element type, that it is dense
-    (pitch: its rows are) and lives on the current device, whose stream the call uses."""
+def _arg(name, t, shape, dtypes, device=None, pitch=False):
+    """The address of an argument of the scoring calls, checked: its shape and element type, that it is dense (pitch:
+    its rows are) and lives on `device`; on the current device, whose stream the call uses, for the call's first."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on a CUDA device")
+        device = torch.cuda.current_device()
+    if t.get_device() != device:
+        raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{device}")
     if pitch:
         if t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: the elements of a row must be adjacent")
@@ -368,13 +376,14 @@ _SCORE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 def _q4_copy(codes, scales):
-    """(address of the codes, of the scales, L, d, group) of a 4-bit copy."""
+    """(address of the codes, of the scales, L, d, group, device) of a 4-bit copy."""
     if codes.dim() != 2 or scales.dim() != 2 or scales.shape[1] < 1:
         raise ValueError("codes must be [L, d / 2] and scales [L, d / group]")
     L, d, n = codes.shape[0], 2 * codes.shape[1], scales.shape[1]
     if d % n:
         raise ValueError(f"{n} scales a row do not divide d = {d}")
-    return _arg("codes", codes, (L, d // 2), _U8), _arg("scales", scales, (L, n), _BF16_BITS), L, d, d // n
+    c, device = _arg("codes", codes, (L, d // 2), _U8), codes.get_device()
+    return c, _arg("scales", scales, (L, n), _BF16_BITS, device), L, d, d // n, device
 
 
 def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales: torch.Tensor, stream=None):
@@ -383,41 +392,42 @@ def elmo_q4_pack(W: torch.Tensor, dtype, group: int, codes: torch.Tensor, scales
     dt = _dt(dtype)
     L, d = W.shape
     group = int(group)
-    _check(load().elmo_q4_pack(_arg("W", W, (L, d), _WEIGHTS[dt]), L, d, dt, group,
-                               _arg("codes", codes, (L, d // 2), _U8),
-                               _arg("scales", scales, (L, d // group if group > 0 else 0), _BF16_BITS),
+    w, device = _arg("W", W, (L, d), _WEIGHTS[dt]), W.get_device()
+    _check(load().elmo_q4_pack(w, L, d, dt, group, _arg("codes", codes, (L, d // 2), _U8, device),
+                               _arg("scales", scales, (L, d // group if group > 0 else 0), _BF16_BITS, device),
                                _stream(stream)))
 
 
 def elmo_q4_unpack(codes: torch.Tensor, scales: torch.Tensor, W: torch.Tensor, stream=None):
     """W (bf16 [L, d]) = the weights that a 4-bit copy stands for."""
-    c, s, L, d, group = _q4_copy(codes, scales)
-    _check(load().elmo_q4_unpack(c, s, L, d, group, _arg("W", W, (L, d), _BF16_BITS), _stream(stream)))
+    c, s, L, d, group, device = _q4_copy(codes, scales)
+    _check(load().elmo_q4_unpack(c, s, L, d, group, _arg("W", W, (L, d), _BF16_BITS, device), _stream(stream)))
 
 
 def elmo_q4_scores(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, Z: torch.Tensor, stream=None):
     """Z (fp32 [B, L], rows may have a pitch) = the scores of the queries X (bf16 [B, d]) against a 4-bit copy."""
-    c, s, L, d, group = _q4_copy(codes, scales)
+    c, s, L, d, group, device = _q4_copy(codes, scales)
     B = X.shape[0]
-    _check(load().elmo_q4_scores(c, s, L, d, group, _arg("X", X, (B, d), _BF16_BITS), B,
-                                 _arg("Z", Z, (B, L), _F32, pitch=True), _pitch(Z), _stream(stream)))
+    _check(load().elmo_q4_scores(c, s, L, d, group, _arg("X", X, (B, d), _BF16_BITS, device), B,
+                                 _arg("Z", Z, (B, L), _F32, device, pitch=True), _pitch(Z), _stream(stream)))
 
 
-def _given(rowptr, cols, B):
+def _given(rowptr, cols, B, device):
     """(address of rowptr, of cols, nnz) of the given labels of B queries."""
     nnz = cols.numel()
-    return _arg("rowptr", rowptr, (B + 1,), _I32), _arg("cols", cols, (nnz,), _I32) if nnz else None, nnz
+    return (_arg("rowptr", rowptr, (B + 1,), _I32, device), _arg("cols", cols, (nnz,), _I32, device) if nnz else None,
+            nnz)
 
 
-def _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp):
+def _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp, device):
     """k and the addresses of the outputs of a log-probability call."""
     if (top_idx is None) != (top_logp is None):
         raise ValueError("top_idx and top_logp go together")
     k = 0 if top_idx is None else top_idx.shape[-1]
-    p = _arg("logp", logp, (nnz,), _F32)
-    return (k, p if nnz else None, _arg("lse", lse, (B,), _F32), _arg("entropy", entropy, (B,), _F32),
-            _arg("top_idx", top_idx, (B, k), _I32) if k else None,
-            _arg("top_logp", top_logp, (B, k), _F32) if k else None)
+    p = _arg("logp", logp, (nnz,), _F32, device)
+    return (k, p if nnz else None, _arg("lse", lse, (B,), _F32, device), _arg("entropy", entropy, (B,), _F32, device),
+            _arg("top_idx", top_idx, (B, k), _I32, device) if k else None,
+            _arg("top_logp", top_logp, (B, k), _F32, device) if k else None)
 
 
 def elmo_score_logprobs_workspace_bytes(B: int, L: int, k: int) -> int:
@@ -435,12 +445,12 @@ def elmo_score_logprobs(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tenso
     with top_logp fp32 [B, k] (None: no list).  workspace: uint8, at least
     elmo_score_logprobs_workspace_bytes(B, L, k) of them; see include/elmo.h."""
     B, L = Z.shape
-    z = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True)
-    rp, cs, nnz = _given(rowptr, cols, B)
-    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
+    z, device = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True), Z.get_device()
+    rp, cs, nnz = _given(rowptr, cols, B, device)
+    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp, device)
     n = workspace.numel()
     _check(load().elmo_score_logprobs(z, _SCORE_TYPES[Z.dtype], _pitch(Z), B, L, rp, cs, nnz, k, p, l, h, ti, tl,
-                                      _arg("workspace", workspace, (n,), _U8), n, _stream(stream)))
+                                      _arg("workspace", workspace, (n,), _U8, device), n, _stream(stream)))
 
 
 def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: torch.Tensor, lse: torch.Tensor,
@@ -450,15 +460,15 @@ def elmo_score_logprobs_backward(Z: torch.Tensor, rowptr: torch.Tensor, cols: to
     """dZ (Z's type and shape; may be Z) = the gradient of elmo_score_logprobs with regard to the scores, given the
     gradients g_logp fp32 [nnz], g_lse and g_entropy fp32 [B] of its outputs (None: zeros) and its lse and entropy."""
     B, L = Z.shape
-    z = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True)
-    rp, cs, nnz = _given(rowptr, cols, B)
-    maybe = lambda name, t, n: None if t is None else _arg(name, t, (n,), _F32)   # noqa: E731
+    z, device = _arg("Z", Z, (B, L), _SCORE_TYPES, pitch=True), Z.get_device()
+    rp, cs, nnz = _given(rowptr, cols, B, device)
+    maybe = lambda name, t, n: None if t is None else _arg(name, t, (n,), _F32, device)   # noqa: E731
     g = maybe("g_logp", g_logp, nnz)
     _check(load().elmo_score_logprobs_backward(z, _SCORE_TYPES[Z.dtype], _pitch(Z), B, L, rp, cs, nnz,
-                                               _arg("lse", lse, (B,), _F32), maybe("entropy", entropy, B),
+                                               _arg("lse", lse, (B,), _F32, device), maybe("entropy", entropy, B),
                                                g if nnz else None, maybe("g_lse", g_lse, B),
                                                maybe("g_entropy", g_entropy, B),
-                                               _arg("dZ", dZ, (B, L), (Z.dtype,), pitch=True), _pitch(dZ),
+                                               _arg("dZ", dZ, (B, L), (Z.dtype,), device, pitch=True), _pitch(dZ),
                                                _stream(stream)))
 
 
@@ -469,10 +479,10 @@ def elmo_label_logprobs(head: Head, X: torch.Tensor, rowptr: torch.Tensor, cols:
     storing a score: logp fp32 [nnz] of the given labels (CSR rowptr / cols), lse and entropy fp32 [B], the k best
     labels top_idx int32 [B, k] with top_logp fp32 [B, k] (None: no list)."""
     B = X.shape[0]
-    rp, cs, nnz = _given(rowptr, cols, B)
-    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp)
-    _check(load().elmo_label_logprobs(head.handle, _arg("X", X, (B, head.d), _BF16_BITS), B, rp, cs, nnz, k, p, l, h, ti,
-                                      tl, _stream(stream)))
+    x, device = _arg("X", X, (B, head.d), _BF16_BITS), X.get_device()
+    rp, cs, nnz = _given(rowptr, cols, B, device)
+    k, p, l, h, ti, tl = _statistics(B, nnz, logp, lse, entropy, top_idx, top_logp, device)
+    _check(load().elmo_label_logprobs(head.handle, x, B, rp, cs, nnz, k, p, l, h, ti, tl, _stream(stream)))
 
 
 def elmo_check_bounded_wait(limit_cycles: int, status: torch.Tensor, stream=None):
