@@ -338,7 +338,9 @@ typedef enum {
   ELMO_K_TOPK_MERGE = 5,  /* top-k merge / exact rescoring */
   ELMO_K_OTHER = 6,       /* fill, clears */
   ELMO_K_STEP = 7,        /* the whole step in one persistent launch: Z, G, dX, dW and the SR update */
-  ELMO_K_COUNT = 8
+  ELMO_K_LOGPROB_SCORE = 8, /* elmo_label_logprobs: scores and their running sums */
+  ELMO_K_LOGPROB_JOIN = 9,  /* elmo_label_logprobs: statistics, given labels, the list */
+  ELMO_K_COUNT = 10
 } elmo_kernel_class;
 
 elmo_status elmo_profile_enable(elmo_head* h, int enable);

@@ -498,7 +498,7 @@ def elmo_sync_status(head: Head, stream=None):
 
 
 KERNEL_CLASSES = {"prep": 0, "logits_grad": 1, "input_grad": 2, "update": 3, "topk_score": 4, "topk_merge": 5,
-                  "other": 6, "step": 7}
+                  "other": 6, "step": 7, "logprob_score": 8, "logprob_join": 9}
 
 
 def elmo_profile_enable(head: Head, enable: bool = True):

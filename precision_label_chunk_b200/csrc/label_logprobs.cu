@@ -1331,13 +1331,13 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   {
-    KernelScope sc(h, ELMO_K_TOPK_SCORE, s, 1);
+    KernelScope sc(h, ELMO_K_LOGPROB_SCORE, s, 1);
     if (!fp8) e = wide ? run_pass<0, 0, 1>(h, A, s) : run_pass<0, 0, 0>(h, A, s);
     else if (h->w_e5m2) e = wide ? run_pass<1, 1, 1>(h, A, s) : run_pass<1, 1, 0>(h, A, s);
     else e = wide ? run_pass<1, 0, 1>(h, A, s) : run_pass<1, 0, 0>(h, A, s);
     if (e != cudaSuccess) return e;
   }
-  KernelScope sc(h, ELMO_K_TOPK_MERGE, s, k == 0 ? 1 : A.streams ? 4 : 2);
+  KernelScope sc(h, ELMO_K_LOGPROB_JOIN, s, k == 0 ? 1 : A.streams ? 4 : 2);
   if (A.fmt == ELMO_BF16) return run_join<ELMO_BF16>(h, A, s);
   if (A.fmt == ELMO_FP8_E5M2) return run_join<ELMO_FP8_E5M2>(h, A, s);
   return run_join<ELMO_FP8_E4M3>(h, A, s);

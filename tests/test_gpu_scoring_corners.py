@@ -163,6 +163,31 @@ def test_products_that_the_tensor_cores_cut_off(grid, L, d):
     h.close()
 
 
+def test_classes_of_their_own_in_the_profile():
+    """The launches of elmo_label_logprobs are told apart from the top-k prediction's."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(13)
+    W, h = head_ops.head_of(elmo, rng.normal(0, 0.02, (20_000, 128)), "e4m3")
+    X = head_ops.bf16(rng.normal(0, 1, (5, 128)))
+    idx, sc = torch.empty(5, 3, dtype=torch.int32, device="cuda"), torch.empty(5, 3, device="cuda")
+    read = lambda: {c: elmo.elmo_profile_read(h, c)[1] for c in elmo.KERNEL_CLASSES}   # noqa: E731
+    elmo.elmo_topk_predict(h, X, 3, 20_000, idx, sc)
+    head_ops.run(elmo, h, X, np.zeros(6, np.int32), np.zeros(0, np.int32), 3)
+    elmo.elmo_profile_enable(h, True)
+    elmo.elmo_topk_predict(h, X, 3, 20_000, idx, sc)
+    alone = read()
+    elmo.elmo_profile_reset(h)
+    elmo.elmo_topk_predict(h, X, 3, 20_000, idx, sc)
+    head_ops.run(elmo, h, X, np.zeros(6, np.int32), np.zeros(0, np.int32), 3)
+    both = read()
+    assert both["topk_score"] == alone["topk_score"] and both["topk_merge"] == alone["topk_merge"]
+    assert both["prep"] == alone["prep"] + 1
+    assert both["logprob_score"] > 0 and both["logprob_join"] > 0
+    assert alone["logprob_score"] == alone["logprob_join"] == 0
+    h.close()
+
+
 # ---------------------------------------------------------------- 4-bit copies
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("L,B", [(300, 1), (300, 9), (300, 30), (40_011, 2), (80_003, 8)])
