@@ -109,7 +109,7 @@ struct Args {
   const uint16_t* X;
   const uint8_t *xa, *xb;                 // 8-bit heads: hi and lo codes [B][d]
   const void* W;
-  int64_t L, label_base, labels_total;
+  int64_t L;
   int32_t d, B, G, k, nnz, fmt, segs;
   int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
   int32_t nblk, nblkp, pairs;             // blocks of a stream, with padding; half tiles of a block
@@ -786,7 +786,7 @@ __device__ __forceinline__ void rank_near(const Args& A, int b, const float* xs,
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += R->ex[j] > z || (R->ex[j] == z && R->el[j] < l);
     if (rank < A.k) {
-      A.top_idx[(size_t)b * A.k + rank] = (int32_t)(l + A.label_base);
+      A.top_idx[(size_t)b * A.k + rank] = l;
       A.top_logp[(size_t)b * A.k + rank] = (float)(z - m - logs);
     }
   }
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   // the score pass still runs elsewhere
   const int e0 = min(max(A.rowptr[b], 0), A.nnz), e1 = min(A.rowptr[b + 1], A.nnz), ee = min(e1, e0 + kEarly);
   auto given = [&](int e) {
-    const int64_t l = (int64_t)A.cols[e] - A.label_base;
+    const int64_t l = A.cols[e];
     return l >= 0 && l < A.L ? exact_score<kFormat>(xs, A.W, l, A.d, lane) : 0.0;
   };
   for (int e = e0 + warp; e < ee; e += kW) {
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
       // no list, or that of a query of zeros (as padding is): every label's score is 0
       if (tid == 0) A.listed[b] = 0;
       for (int i = tid; i < A.k; i += kJoinThreads) {
-        A.top_idx[(size_t)b * A.k + i] = bad ? -1 : (int32_t)(i + A.label_base);
+        A.top_idx[(size_t)b * A.k + i] = bad ? -1 : i;
         A.top_logp[(size_t)b * A.k + i] = bad ? -INFINITY : (float)(0.0 - m - logs);
       }
     } else {
@@ -977,13 +977,13 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   }
 
   auto put = [&](int e, double z) {
-    const int64_t id = A.cols[e], l = id - A.label_base;
+    const int32_t l = A.cols[e];
     float r = (float)(z - m - logs);
-    if (id < 0 || id >= A.labels_total) {
+    if (l < 0 || l >= A.L) {
       r = NAN;
       if (atomicCAS(A.status, 0, (int)ELMO_EDATA) == 0) A.status[1] = e;
-    } else if (l < 0 || l >= A.L || (z == -INFINITY && !isnan(m + logs))) {
-      r = -INFINITY;                                   // another device's label, or a masked one
+    } else if (z == -INFINITY && !isnan(m + logs)) {
+      r = -INFINITY;                                   // a masked label
     }
     A.logp[e] = r;
   };
@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
       int32_t l = 0;
       if (pk != 0) best_after(A.segs * A.k, at, pk, pi, rk, ri, k, l);
       if (tid == 0) {
-        A.top_idx[(size_t)b * A.k + q] = k ? (int32_t)(l + A.label_base) : -1;
+        A.top_idx[(size_t)b * A.k + q] = k ? l : -1;
         A.top_logp[(size_t)b * A.k + q] = k ? (float)(ord64_value(k) - m - logs) : -INFINITY;
       }
       pk = k;
@@ -1294,8 +1294,6 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.xb = ws + o.xb;
   A.W = h->W;
   A.L = h->L;
-  A.label_base = h->label_base;
-  A.labels_total = h->labels_total;
   A.d = h->d; A.B = B; A.G = o.G; A.k = k; A.nnz = nnz;
   A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.streams = o.streams;
   A.fmt = w_format(h);
