@@ -560,7 +560,7 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
  * are formed from tensor-core scores (fp32 accumulation; in 8-bit heads X
  * enters as a sum of two 8-bit numbers, which holds every bf16 value above
  * 2^-13 of its query's largest magnitude exactly and the others to within
- * 2^-21 of it); the scores of the
+ * 2^-21 of it, or 2^-140 if that is more); the scores of the
  * given and of the listed labels are exact products summed in 64 bits, and the
  * k best labels are those of these exact scores, ties to the lower label.
  * (elmo_topk_predict ranks by an fp32 chain: the two lists may differ where

@@ -9,7 +9,7 @@
 //
 //   1. operands: bf16 heads multiply X as it is.  8-bit heads multiply
 //      X = (hi + lo) / s_b: s_b a power of two for each query with
-//      s_b max|x| in (224, 448] (s_b at most 2^60), hi = rne_e4m3(s_b x), lo = rne_e5m2(s_b x - hi).
+//      s_b max|x| in (224, 448] (s_b at most 2^126), hi = rne_e4m3(s_b x), lo = rne_e5m2(s_b x - hi).
 //      A bf16 number has 8 significant bits, hi takes 4 and leaves at most 8
 //      units of the last place, which E5M2's 3 bits hold exactly.  Only below
 //      E4M3's normal numbers, 2^-6 and so at most 2^-13 of the query's largest,
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
   if (kFp8 && !bad && m != 0) {
     int e2;
     const float f = frexpf(__uint_as_float(m << 16), &e2);
-    // 448 = 0.875 2^9; at most 2^60, so that the accumulators' -200 / inv stays finite
-    s = ldexpf(1.0f, max(-126, min(60, f <= 0.875f ? 9 - e2 : 8 - e2)));
+    // 448 = 0.875 2^9; at most 2^126, so that 1 / s is a normal number
+    s = ldexpf(1.0f, max(-126, min(126, f <= 0.875f ? 9 - e2 : 8 - e2)));
   }
   float n = 0.0f, r = 0.0f;
   for (int j = tid; j < A.d / 2; j += kPrepThreads) {

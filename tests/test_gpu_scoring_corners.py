@@ -163,6 +163,22 @@ def test_products_that_the_tensor_cores_cut_off(grid, L, d):
     h.close()
 
 
+@pytest.mark.parametrize("grid", ["bf16", "e4m3", "e5m2"])
+def test_small_queries(grid):
+    """Queries down to the smallest magnitudes beside ordinary ones: statistics and lists of each."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(17)
+    L, d, k = 20_011, 128, 5
+    W, h = head_ops.head_of(elmo, rng.normal(0, 4, (L, d)), grid)
+    x = rng.normal(0, 1, (7, d)) * 2.0 ** np.array([0, -45, -55, -70, -90, -110, -118])[:, None]
+    X = head_ops.bf16(x)
+    rowptr, cols = head_ops.lists(rng, 7, L, 3)
+    head_ops.check(head_ops.run(elmo, h, X, rowptr, cols, k), X.double().cpu().numpy(), W.double().cpu().numpy(), grid,
+                   rowptr, cols, k)
+    h.close()
+
+
 def test_classes_of_their_own_in_the_profile():
     """The launches of elmo_label_logprobs are told apart from the top-k prediction's."""
     need_gpu()
