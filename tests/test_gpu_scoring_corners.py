@@ -53,6 +53,42 @@ def test_rows_with_nan_beside_infinity(dtype, L):
     assert np.isnan(dz[spoiled]).all() and (dz[[n, n + 1, n + 3]] == 0).all()
 
 
+@pytest.mark.parametrize("op", ["scores", "head"])
+def test_bad_row_pointers_write_their_own_entries_only(op):
+    """Row pointers that lie outside [0, nnz) or run backwards: entries of the rows that remain are right, all others and
+    what lies around the array are left as they were."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(0)
+    L, d, nnz, guard = 500, 64, 6, 64
+    cols = np.array([499, 3, 250, 7, 7, 0], np.int32)
+    W, h = head_ops.head_of(elmo, rng.normal(0, 0.1, (L, d)), "bf16")
+    X = head_ops.bf16(rng.normal(0, 1, (3, d)))
+    z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+    Z = torch.from_numpy(z.astype(np.float32)).cuda()
+    want = z - np.log(np.exp(z).sum(1, keepdims=True))
+    work = torch.empty(elmo.elmo_score_logprobs_workspace_bytes(3, L, 2), dtype=torch.uint8, device="cuda")
+    for ptr in ([-3, 2, 1, 99], [9, 8, 7, 6], [0, 2**31 - 1, -2**31, 2], [2, 4, 4, 5], [6, 6, 0, 3]):
+        whole = torch.full((nnz + 2 * guard,), 55.0, device="cuda")
+        out = (whole[guard:guard + nnz], *head_ops.buffers(3, 0, 2)[1:])
+        lists = torch.tensor(ptr, dtype=torch.int32).cuda(), torch.from_numpy(cols).cuda()
+        if op == "scores":
+            elmo.elmo_score_logprobs(Z, *lists, *out, work)
+        else:
+            elmo.elmo_label_logprobs(h, X, *lists, *out)
+            elmo.elmo_sync_status(h)
+        got = whole.cpu().numpy()
+        assert (got[:guard] == 55).all() and (got[guard + nnz:] == 55).all(), ptr
+        rows = [(max(ptr[b], 0), min(ptr[b + 1], nnz)) for b in range(3)]
+        for e in range(nnz):
+            owners = [b for b, (e0, e1) in enumerate(rows) if e0 <= e < e1]
+            if not owners:
+                assert got[guard + e] == 55, (ptr, e)
+            else:                                               # an entry of two rows has either one's
+                assert min(abs(got[guard + e] - want[b, cols[e]]) for b in owners) < 1e-4, (ptr, e)
+    h.close()
+
+
 # ---------------------------------------------------------------- heads
 @pytest.mark.parametrize("grid,d", [("bf16", 128), ("bf16", 832), ("e5m2", 128), ("e5m2", 832)])
 @pytest.mark.parametrize("L", [2000, 60_000])
@@ -179,6 +215,63 @@ def test_small_queries(grid):
     h.close()
 
 
+@pytest.mark.parametrize("grid,outlier", [("e4m3", 448.0), ("bf16", 1e4), ("e5m2", 57344.0)])
+def test_one_weight_far_above_the_others(grid, outlier):
+    """The bound of the list goes with the largest weight of the head: one outlier sends the queries to the exact path."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(23)
+    L, d, B, k = 60_000, 768, 5, 5
+    w = rng.normal(0, 0.02, (L, d))
+    w[41_234, 5] = outlier
+    W, h = head_ops.head_of(elmo, w, grid)
+    x = rng.normal(0, 1, (B, d))
+    x[2, 5] = 0                                                 # the outlier's label is an ordinary one of this query
+    X = head_ops.bf16(x)
+    z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+    idx = head_ops.run(elmo, h, X, np.zeros(B + 1, np.int32), np.zeros(0, np.int32), k)[3]
+    assert np.array_equal(idx, np.argsort(-z, 1, kind="stable")[:, :k])
+    h.close()
+
+
+@pytest.mark.parametrize("grid,L,d,pairs", [("bf16", 600_011, 64, 2), ("e4m3", 600_011, 64, 2), ("e4m3", 1_100_003, 64, 4),
+                                            ("bf16", 1_048_577, 128, 4), ("e5m2", 1_060_001, 832, 2)])
+def test_blocks_of_several_tiles(grid, L, d, pairs):
+    """Heads and batches so large that a block's maximum stands for several half tiles (4096 queries x L / 64 tiles, or
+    / 128 of wide heads, of maxima pass 256 MB): the best labels are found wherever they lie, in the last, partial blocks
+    of every stream among others."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    B, k = 4096, 8
+    g = torch.Generator(device="cuda").manual_seed(L)
+    W = torch.randn(L, d, generator=g, device="cuda") * 0.02
+    W[-700:] *= 1.6                                             # many of the best are among the last labels,
+    W[::1009] *= 1.5                                            # the others spread over all places in a block
+    W = W.to(head_ops.GRIDS[grid])
+    X = torch.randn(B, d, generator=g, device="cuda").to(torch.bfloat16)
+    rng = np.random.default_rng(L)
+    rowptr, cols = head_ops.lists(rng, B, L, 1)
+    h = elmo.elmo_init_head(W, grid)
+    logp, lse, H, idx, top = head_ops.run(elmo, h, X, rowptr, cols, k)
+    pick = np.r_[0, 1, 127, 128, 300:310, 2047, 2048, 4000:4004, B - 2, B - 1]
+    Z = torch.cat([X[torch.from_numpy(pick).cuda()].double() @ W[a:a + 100_000].double().T for a in range(0, L, 100_000)], 1)
+    want = torch.logsumexp(Z, 1)
+    p = torch.exp(Z - want[:, None])
+    wH = -(p * (Z - want[:, None])).sum(1)
+    steps = (1 if grid == "bf16" else 2) * -(-d * (2 if grid == "bf16" else 1) // 128) * 4
+    dz = steps * 2.0**-22 * float((X[:200].double().abs() @ W[-2000:].double().abs().T).max()) * 1.2
+    assert np.abs(lse[pick] - want.cpu().numpy()).max() < dz + 2e-5
+    assert np.abs(H[pick] - wH.cpu().numpy()).max() < 4 * dz + 1e-4
+    wt, wi = torch.topk(Z, k, 1)
+    assert np.array_equal(idx[pick], wi.int().cpu().numpy())
+    assert (wi >= L - 700).sum() > 20 and (wi < L - 700).sum() > 20
+    assert np.abs(top[pick] - (wt - want[:, None]).cpu().numpy()).max() < dz + 2e-5
+    for i, b in enumerate(pick):
+        at = (Z[i, torch.from_numpy(cols[rowptr[b]:rowptr[b + 1]]).long().cuda()] - want[i]).cpu().numpy()
+        assert (np.abs(logp[rowptr[b]:rowptr[b + 1]] - at) < dz + 2e-5).all(), b
+    h.close()
+
+
 def test_classes_of_their_own_in_the_profile():
     """The launches of elmo_label_logprobs are told apart from the top-k prediction's."""
     need_gpu()
@@ -231,3 +324,24 @@ def test_scores_of_large_scales(group, L, B):
     assert (got[over] == np.sign(z[over]) * INF).all()
     scaled = np.abs(z) * 2.0 ** (14 - np.floor(np.log2(np.abs(x).max(1))))[:, None]
     assert (scaled > most)[holds].mean() > 0.1                  # with each query's largest element in [2^14, 2^15)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("L,d,B", [(80_003, 128, 8), (75_776, 192, 1), (76_001, 256, 5)])
+def test_scores_with_two_label_blocks_a_warp(group, L, d, B):
+    """Few queries and labels for every SM twice over: all labels of the last, partial tiles among the others."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    if d % group:
+        d += 64
+    rng = np.random.default_rng(L + group)
+    u = rng.integers(0, 16, (L, d)).astype(np.uint8)
+    s = q4_ops.bf16_of(np.abs(rng.normal(0, 0.01, (L, d // group))))
+    x = q4_ops.bf16_of(rng.normal(0, 1, (B, d)))
+    Z = torch.full((B, L + 1), 123.0, device="cuda")
+    elmo.elmo_q4_scores(torch.from_numpy(q4_ops.nibbles(u)).cuda(), torch.from_numpy(s).to(torch.bfloat16).cuda(),
+                        torch.from_numpy(x).to(torch.bfloat16).cuda(), Z[:, :L])
+    z, mag = q4_ops.scored(u, s, x, group)
+    got = Z.double().cpu().numpy()
+    assert (got[:, L:] == 123.0).all()
+    assert (np.abs(got[:, :L] - z) <= q4_ops.tolerance(d, group) * mag + np.abs(z) * 2.0**-24).all()
