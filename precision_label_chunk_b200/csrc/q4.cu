@@ -227,9 +227,12 @@ cudaError_t run_pack(const void* W, int64_t n8, int32_t group, uint32_t* codes, 
 // its largest magnitude into [2^14, 2^15).  A bf16 number's 8 bits fit fp16's
 // 11; numbers below 2^-31 of the query's largest are rounded, to within 2^-39
 // of it, which is far below the fp32 sums' own rounding.
-// The scaling is undone last, so that under scales of 2^100 and more the sums may
-// overflow where the score does not: a score that is not finite, of a query that
-// is, is formed again in 64 bits.
+// The scaling is undone last, so that the sums may overflow where the score does
+// not.  They stay below d 2^18 times the label's largest scale, so only scales of
+// 2^97 and more can do that: q4_scores_again (3M labels x 768, all scales so
+// large: 1.7 ms for 1 query, 37 for 32).  Where it stands matters, and that
+// nothing of it lives on in the loop over the tiles: called from that loop it
+// cost registers, 124 us for 500K labels and 32 queries in place of 109.
 //
 // Bound by the read of the codes and the unpacking together (1M labels: DRAM
 // 56 %, issue slots 60 %): on B200, 3M labels x 768 in groups of 64 and one query
@@ -241,6 +244,7 @@ constexpr int kQKB = 128;                 // bytes of a box's row: 256 codes
 constexpr int kQMaxStages = 8;
 constexpr long long kQWait = 4000000000LL;
 constexpr size_t kQSmem = 225 * 1024;     // of the 227 KB a CTA may have
+constexpr uint32_t kQLarge = (97 + 127) << 7;   // 2^97 in bf16
 constexpr int kQMaxNB = 4;                // 8-query column blocks of one pass
 
 template <int kG> __device__ __forceinline__ int q4_row(int g) {
@@ -323,7 +327,8 @@ __device__ __forceinline__ void pow2_factors(int e, float& f0, float& f1) {
 struct SmemQ {
   uint64_t full[kQMaxStages], empty[kQMaxStages];
   int32_t exponent[8 * kQMaxNB];
-  int32_t finite[8 * kQMaxNB];
+  int32_t finite[8 * kQMaxNB];          // whether the query is
+  volatile int odd[17];                 // whether a warp has met a sum that is not finite
   int abort;
 };
 
@@ -345,34 +350,34 @@ struct Q4Args {
   int32_t d, B, stages;
 };
 
-// The scores that a thread has stored, label0 and those 8 apart from it, of
-// queries 8 nb + 2 t and the next: those that are not finite again in 64 bits,
-// where the query is.
-template <int kG>
-__device__ __noinline__ void q4_scores_again(const Q4Args& A, const int32_t* finite, int64_t label0, int labels, int b0,
-                                             int nbs, int t) {
-  for (int nb = 0; nb < nbs; ++nb) {
-    for (int c = 0; c < 2; ++c) {
-      const int n = nb * 8 + 2 * t + c;
-      if (b0 + n >= A.B || !finite[n]) continue;
-      for (int i = 0; i < labels; ++i) {
-        const int64_t l = label0 + 8 * i;
-        float* to = A.Z + (int64_t)(b0 + n) * A.ldz + l;
-        if (l >= A.L || fabsf(*to) < INFINITY) continue;
-        const uint8_t* codes = A.codes + l * (A.d / 2);
-        const uint16_t* scales = A.scales + l * (A.d / kG);
-        const uint16_t* x = A.X + (size_t)(b0 + n) * A.d;
-        double z = 0.0;
-        for (int g = 0; g < A.d / kG; ++g) {
-          double sum = 0.0;
-          for (int j = g * kG; j < (g + 1) * kG; j += 8) {
-            const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(codes + j / 2));
-            for (int e = 0; e < 8; ++e) sum += (double)bf16_to_f32(x[j + e]) * ((int)(u >> (4 * e) & 15u) - 8);
-          }
-          z += (double)bf16_to_f32(scales[g]) * sum;
+// After the last tile, for a warp that has met a sum that is not finite: the
+// scores of its labels with a scale of kQLarge or more that are not finite, of
+// queries and scales that are, again in 64 bits.
+template <int kG, int kRows, int kTile>
+__device__ __noinline__ void q4_scores_again(const Q4Args A, const int32_t* finite, int queries) {
+  const int lane = threadIdx.x & 31, b0 = blockIdx.y * queries;
+  for (int64_t tile = (int64_t)blockIdx.x * kTile; tile < A.L; tile += (int64_t)gridDim.x * kTile) {
+    const int64_t l = tile + (threadIdx.x >> 5) * kRows + lane % kRows;
+    if (l >= A.L) continue;
+    const uint8_t* codes = A.codes + l * (A.d / 2);
+    const uint16_t* scales = A.scales + l * (A.d / kG);
+    uint32_t most = 0;
+    for (int g = 0; g < A.d / kG; ++g) most = max(most, scales[g] & 0x7FFFu);
+    if (most < kQLarge || most >= 0x7F80u) continue;
+    for (int n = lane / kRows; n < queries && b0 + n < A.B; n += 32 / kRows) {
+      float* to = A.Z + (int64_t)(b0 + n) * A.ldz + l;
+      if (!finite[n] || fabsf(*to) < INFINITY) continue;
+      const uint16_t* x = A.X + (size_t)(b0 + n) * A.d;
+      double z = 0.0;
+      for (int g = 0; g < A.d / kG; ++g) {
+        double sum = 0.0;
+        for (int j = g * kG; j < (g + 1) * kG; j += 8) {
+          const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(codes + j / 2));
+          for (int e = 0; e < 8; ++e) sum += (double)bf16_to_f32(x[j + e]) * ((int)(u >> (4 * e) & 15u) - 8);
         }
-        *to = (float)z;
+        z += (double)bf16_to_f32(scales[g]) * sum;
       }
+      *to = (float)z;
     }
   }
 }
@@ -382,7 +387,7 @@ __device__ __noinline__ void q4_scores_again(const Q4Args& A, const int32_t* fin
 // one for the TMA.
 template <int kG, int kMT, int kNB, int kWarps>
 __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
-    q4_scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Q4Args A) {
+    q4_scores_kernel(const __grid_constant__ CUtensorMap tmQ, const Q4Args A) {
   constexpr int kRows = 16 * kMT;                    // labels of a warp
   constexpr int kTile = kRows * kWarps;              // labels of a tile
   constexpr uint32_t kStage = kTile * kQKB;
@@ -404,6 +409,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < A.stages; ++s) { mbar_init(&S->full[s], 1); mbar_init(&S->empty[s], kWarps); }
     S->abort = 0;
+    for (int w = 0; w <= kWarps; ++w) S->odd[w] = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
     const int row0 = warp * kRows + q4_row<kG>(g);     // of the tile: fragment rows g, g + 8 are rows row0, row0 + 8
     // byte t kG / 8 of a row's group j, swizzled; rows row0 + 8 i share row & 7
     const uint32_t mine = smem_u32(ring) + (uint32_t)row0 * kQKB, swz = (uint32_t)(row0 & 7) << 4;
-    float odd = 0.0f;                                  // NaN once a score is not finite
+    float odd = 0.0f;                                  // NaN from the first sum that is not finite on
     for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x, buf ^= 1) {
       cp_async_wait();
       __syncwarp();
@@ -581,9 +587,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
           for (int r = lane; r < kRows; r += 32)
             for (int n = b0; n < min(b0 + 8 * kNB, A.B); ++n)
               if (tl * kTile + warp * kRows + r < A.L) A.Z[(int64_t)n * A.ldz + tl * kTile + warp * kRows + r] = NAN;
-        odd = 0.0f;
         break;
       }
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb)
+          odd = __fmaf_rn((out[m][nb][0] + out[m][nb][1]) + (out[m][nb][2] + out[m][nb][3]), 0.0f, odd);
 #pragma unroll
       for (int nb = 0; nb < kNB; ++nb) {
 #pragma unroll
@@ -599,20 +609,16 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               if (16 * m + 8 * h < left) {
-                const float v = out[m][nb][2 * h + c] * f0 * f1;
-                __stcs(z + 16 * m + 8 * h, v);
-                odd = __fmaf_rn(v, 0.0f, odd);
+                __stcs(z + 16 * m + 8 * h, out[m][nb][2 * h + c] * f0 * f1);
               }
           }
         }
       }
     }
-    // after the tiles: a call among them costs registers (500K labels, 32 queries: 107 us against 124)
-    if (odd != 0.0f)
-      for (int64_t tile = blockIdx.x; tile < T; tile += gridDim.x)
-        q4_scores_again<kG>(A, S->finite, tile * kTile + row0, 2 * kMT, b0, kNB, t);
+    if (odd != 0.0f) S->odd[warp] = 1;
   }
   __syncthreads();
+  if (S->odd[warp] && !*abort) q4_scores_again<kG, kRows, kTile>(A, S->finite, 8 * kNB);
   if (*abort) __nanosleep(20000);       // copies still in flight land before the shared memory is given up
 }
 
