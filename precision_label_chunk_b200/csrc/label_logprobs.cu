@@ -65,6 +65,7 @@
 #include "elmo_operators.h"
 #include "softmax.cuh"
 #include "tc_ptx.cuh"
+#include "weights8.cuh"
 
 namespace elmo {
 namespace {
@@ -592,11 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- exact scores
-// Eight weights of a label from element 8 c on, as they are stored; kFormat is
-// the head's format, so that a loop's loads all start before the first is used.
-template <int kFormat> struct Raw8 { uint2 v; };
-template <> struct Raw8<ELMO_BF16> { uint4 v; };
-
+// Eight weights of a label from element 8 c on, as they are stored: a loop's
+// loads all start before the first is used.
 template <int kFormat>
 __device__ __forceinline__ Raw8<kFormat> load8(const void* W, int64_t l, int d, int c) {
   Raw8<kFormat> r;
@@ -604,24 +602,6 @@ __device__ __forceinline__ Raw8<kFormat> load8(const void* W, int64_t l, int d, 
   else r.v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(W) + l * d) + c);
   return r;
 }
-template <int kFormat>
-__device__ __forceinline__ void values8(const Raw8<kFormat>& r, float (&f)[8]) {
-  if constexpr (kFormat == ELMO_BF16) {
-    const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(u[e] << 16);
-      f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-    }
-  } else {
-    float a[4], b[4];
-    if constexpr (kFormat == ELMO_FP8_E5M2) { e5m2x4_to_f32(r.v.x, a); e5m2x4_to_f32(r.v.y, b); }
-    else { e4m3x4_to_f32(r.v.x, a); e4m3x4_to_f32(r.v.y, b); }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { f[e] = a[e]; f[4 + e] = b[e]; }
-  }
-}
-
 // x . w_l with exact products and sums in 64 bits, by one warp, in an order
 // that depends on d alone: equal rows have equal scores.
 template <int kFormat>

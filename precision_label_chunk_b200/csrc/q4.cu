@@ -18,6 +18,7 @@
 #include "elmo_internal.h"
 #include "elmo_operators.h"
 #include "tc_ptx.cuh"
+#include "weights8.cuh"
 
 namespace elmo {
 namespace {
@@ -47,27 +48,6 @@ using namespace tc;
 // those in groups of 64: 160 us to pack (6.1 TB/s), 156 us to unpack (6.3 TB/s).
 constexpr int kPackThreads = 256;
 constexpr int kPackAt = 4;
-
-template <int kFormat> struct Raw8 { uint2 v; };
-template <> struct Raw8<ELMO_BF16> { uint4 v; };
-
-template <int kFormat>
-__device__ __forceinline__ void values8(const Raw8<kFormat>& r, float (&w)[8]) {
-  if constexpr (kFormat == ELMO_BF16) {
-    const uint32_t v[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      w[2 * e] = __uint_as_float(v[e] << 16);
-      w[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-    }
-  } else {
-    float a[4], b[4];
-    if constexpr (kFormat == ELMO_FP8_E5M2) { e5m2x4_to_f32(r.v.x, a); e5m2x4_to_f32(r.v.y, b); }
-    else { e4m3x4_to_f32(r.v.x, a); e4m3x4_to_f32(r.v.y, b); }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { w[e] = a[e]; w[4 + e] = b[e]; }
-  }
-}
 
 // the largest magnitude's code of eight weights, and a code's value
 template <int kFormat> __device__ __forceinline__ uint32_t code_max(const Raw8<kFormat>& r) {
