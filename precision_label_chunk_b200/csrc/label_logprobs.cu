@@ -39,16 +39,24 @@
 //      bf16 labels x 768 and one query, 0.87 for 4; 21 ms for 3M E4M3 labels
 //      and 16.
 //
-// delta = (gamma (n1 + r1) + r1) max|W|, n1 = sum_j (|hi| + |lo|) / s_b,
-// r1 the sum of what hi and lo leave.  gamma = 2^-24 times the products that
-// the accumulating instructions add (16 each of 16-bit, 32 of 8-bit operands).
-// How these round is documented nowhere.  Measured on B200, an instruction
+// delta = (eps nw + r1) max|W|, r1 the sum of what hi and lo leave.  How the
+// accumulating instructions round is documented nowhere.  Measured on B200, one
 // cuts each product at 2^-25 of the largest addend, the sum so far among them,
 // and the sum to fp32: crafted queries lost 2^-21.0 of the magnitudes summed an
-// instruction of 16 products and 2^-20.0 of 32, where gamma allows 2^-20 and
-// 2^-19 (2^-22 puts such labels in the wrong order).  A
-// thirty-second of the fp32 sum's d terms and 5 joins are less.  max|W| is
-// read off the tiles in shared memory by two spare warps.
+// instruction of 16 products (16-bit operands) and 2^-20.0 of 32 (8-bit).  eps
+// allows half as much again, 1.5 2^-25 a product (2^-22 an instruction puts such
+// labels in the wrong order).  An element of X counts for the instructions
+// from its own on, nw = sum_j (|hi| n(hi_j) + |lo| n(lo_j)) / s_b with n that
+// number: a cut is one of the sum so far.  (Every element for every
+// instruction, and as much for the fp32 scores, sent 64 queries against 1M
+// E4M3 labels x 4096, 64 best, to the exact path: 61 ms in place of 1.6.)
+// The fp32 scores are off by 2^-24 of the magnitudes for each addition of a
+// chain: d / 32 products a lane and 5 joins.  max|W| is read off the tiles in
+// shared memory by two spare warps.  One weight far above the others widens
+// delta for every label, and from some hundred times their deviation on queries
+// go to the exact path: with a deviation of 0.02, one weight of 8 costs 3M E4M3
+// labels x 768 nothing, one of 448 takes 16 queries from 0.5 to 22 ms; x 2048,
+// one of 4 takes 4 queries from 2.9 to 13 ms.
 //
 // Bounds and times on B200.  Few queries: the read of W; 500K bf16 labels x
 // 768, 4 queries: pass 126 us (6.1 TB/s), all of it 158.  Many: the MMAs, most
@@ -84,7 +92,7 @@ constexpr int64_t kKeepLabels = 16384;    // heads of up to so many labels keep 
 constexpr size_t kKeepBytes = size_t(64) << 20;   // if they take no more than this
 constexpr int kJoinThreads = 512;
 constexpr int kGroups = 256;              // groups whose best give the lower bound on the k-th best
-constexpr int kMaxBlocks = 256;           // blocks that are scored again for a query,
+constexpr int kMaxBlocks = 2048;          // blocks that are scored again for a query,
 constexpr int kMaxNear = 4096;            // of their labels the ones near the k-th best in fp32,
 constexpr int kMaxExact = 1024;           // and of those the ones ranked by exact scores
 constexpr int kNearThreads = 256;
@@ -115,8 +123,8 @@ struct Args {
   int32_t q, kbs, stages, kb3d;           // tiles and k-blocks of a stage; one TMA request for all of them
   int32_t nblk, nblkp, pairs;             // blocks of a stream, with padding; half tiles of a block
   int32_t streams;                        // kStreams; 0 where every label's score is kept: nblkp is their pitch
-  float gamma;
-  float *xinv, *n1, *r1;
+  float eps;                              // what an instruction may lose of the magnitudes it has summed
+  float *xinv, *n1, *nw, *r1;
   int32_t *rflag, *fail;
   int32_t* done;                          // [B] segments of a failed query that are ranked
   Counts* counts;
@@ -180,8 +188,12 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
     // 448 = 0.875 2^9; at most 2^126, so that 1 / s is a normal number
     s = ldexpf(1.0f, max(-126, min(126, f <= 0.875f ? 9 - e2 : 8 - e2)));
   }
-  float n = 0.0f, r = 0.0f;
+  // 32 bytes of K an instruction: element k's hi is in instruction 4 ops (k / kKE) + k % kKE / (kKE / 4), its lo 4 later
+  constexpr int kKE = kFp8 ? 128 : 64, kOps = kFp8 ? 2 : 1;
+  const int steps = (A.d + kKE - 1) / kKE * 4 * kOps;
+  float n = 0.0f, nw = 0.0f, r = 0.0f;
   for (int j = tid; j < A.d / 2; j += kPrepThreads) {
+    const float from = (float)(steps - 2 * j / kKE * 4 * kOps - 2 * j % kKE / (kKE / 4));   // instructions from hi's own on
     const uint32_t w = xr[j];
     uint32_t hi2 = 0, lo2 = 0;
 #pragma unroll
@@ -195,11 +207,13 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
         const uint32_t cl = pack_e5m2x2(0.0f, left) & 0xFFu;
         const float lo = e5m2_to_f32((uint8_t)cl);
         n = __fadd_ru(n, __fadd_ru(fabsf(hi), fabsf(lo)));
+        nw = __fmaf_ru(fabsf(hi), from, __fmaf_ru(fabsf(lo), from - 4.0f, nw));
         r = __fadd_ru(r, fabsf(__fsub_rn(left, lo)));
         hi2 |= ch << (8 * h);
         lo2 |= cl << (8 * h);
       } else {
         n = __fadd_ru(n, fabsf(x));
+        nw = __fmaf_ru(fabsf(x), from, nw);
       }
     }
     if (kFp8) {
@@ -208,11 +222,13 @@ __global__ void __launch_bounds__(kPrepThreads) label_prep_kernel(const Args A, 
     }
   }
   n = block_sum_up(n, red);
+  nw = block_sum_up(nw, red);
   r = block_sum_up(r, red);
   if (tid == 0) {
     const float inv = 1.0f / s;                              // exact
     A.xinv[b] = inv;
     A.n1[b] = __fmul_ru(n, inv);
+    A.nw[b] = __fmul_ru(nw, inv);
     A.r1[b] = __fmul_ru(r, inv);
     A.rflag[b] = bad ? 1 : 0;
   }
@@ -499,12 +515,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mx = max32(v);
           best = fmaxf(best, mx);
           soft.add32(v, mx, [&](float (&bad)[32]) {
-            if (!kW5 || !finite) return false;
+            if constexpr (kW5) {
+              if (!finite) return false;
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (bad[c] != bad[c])
-                bad[c] = infinite_score(A.X + (size_t)row * A.d, static_cast<const uint8_t*>(A.W) + (size_t)(l0 + c) * A.d, A.d);
-            return true;
+              for (int c = 0; c < 32; ++c)
+                if (bad[c] != bad[c])
+                  bad[c] = infinite_score(A.X + (size_t)row * A.d, static_cast<const uint8_t*>(A.W) + (size_t)(l0 + c) * A.d, A.d);
+              return true;
+            }
+            return false;
           });
           if (keep) {
 #pragma unroll
@@ -711,18 +730,22 @@ __device__ __forceinline__ float lower_bound_kth(SmemB* S, float best, int k) {
   return S->low;
 }
 
-// 2 delta of a query, rounded up; 2^-126 for subnormal partial sums.  Infinite
-// where the weights are not finite or a sum may leave fp32's range on its way
-// (to an infinity or a NaN that no bound holds for).
-__device__ __forceinline__ float two_delta(const Args& A, int b) {
-  const float n = __fadd_ru(A.n1[b], A.r1[b]), w = max_weight(A.counts->wmax, A.fmt);
-  if (!(__fmul_ru(n, w) < 0x1p126f)) return INFINITY;
-  const float d = __fmul_ru(__fadd_ru(__fmul_ru(A.gamma, n), A.r1[b]), w);
-  return __fmul_ru(2.0f, __fadd_ru(d, 0x1p-126f));
+// The error bounds of a query's scores, rounded up; 2^-126 for subnormal partial
+// sums: `tensor` of the tensor cores', `near` of the fp32 ones.  Infinite where
+// the weights are not finite or a sum may leave fp32's range on its way (to an
+// infinity or a NaN that no bound holds for).
+struct Deltas { float tensor, near; };
+__device__ __forceinline__ Deltas deltas_of(const Args& A, int b) {
+  const float r = A.r1[b], n = __fadd_ru(A.n1[b], r), w = max_weight(A.counts->wmax, A.fmt);
+  const float all = __fmul_ru(n, w);
+  if (!(all < 0x1p126f)) return {INFINITY, INFINITY};
+  const float chain = (float)((A.d + 255) / 256 * 8 + 6) * 0x1p-24f;     // an addition more for what the others' rounding adds
+  return {__fadd_ru(__fmul_ru(__fmaf_ru(A.eps, A.nw[b], r), w), 0x1p-126f), __fadd_ru(__fmul_ru(chain, all), 0x1p-126f)};
 }
 
 // Ranks a query's `near` labels near the k-th best by exact scores, or lists the
-// query for the exact path.  The whole CTA.
+// query for the exact path; their scores in near_v are off by `delta` at most.
+// The whole CTA.
 struct SmemR {
   double ex[kMaxExact];
   int32_t el[kMaxExact];
@@ -730,17 +753,16 @@ struct SmemR {
 };
 
 template <int kFormat, int kThr>
-__device__ __forceinline__ void rank_near(const Args& A, int b, const float* xs, int near, double m, double logs, SmemB* S,
-                                          SmemR* R) {
+__device__ __forceinline__ void rank_near(const Args& A, int b, const float* xs, int near, float delta, double m, double logs,
+                                          SmemB* S, SmemR* R) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool ok = near >= A.k && near <= kMaxNear;
   const float* nv = A.near_v + (size_t)b * kMaxNear;
   if (tid == 0) R->nexact = 0;
   if (ok) {
-    const float two = two_delta(A, b);
     float best = -INFINITY;
     for (int i = tid; i < near; i += kThr) best = fmaxf(best, nv[i]);
-    const float cut = __fsub_rd(lower_bound_kth<kThr>(S, best, A.k), two);
+    const float cut = __fsub_rd(lower_bound_kth<kThr>(S, best, A.k), __fmul_ru(2.0f, delta));
     for (int i = tid; i < near; i += kThr) {
       if (nv[i] >= cut) {
         const int at = atomicAdd(&R->nexact, 1);
@@ -789,8 +811,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   extern __shared__ __align__(16) uint8_t dyn[];
   float* xs = reinterpret_cast<float*>(dyn);           // [d] the query
   __shared__ SmemB S;
-  __shared__ SmemR R;
-  __shared__ int32_t blocks[kMaxBlocks];
+  __shared__ union { SmemR rank; int32_t blocks[kMaxBlocks]; } U;   // one or the other
   constexpr int kW = kJoinThreads / 32;
   constexpr int kEarly = 512;
   __shared__ double stat[2], ws[kW], wt[kW], early[kEarly];
@@ -871,7 +892,8 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
   const double m = stat[0], logs = stat[1];
 
   if (A.k > 0) {
-    const float two = two_delta(A, b), inv = A.xinv[b];
+    const Deltas delta = deltas_of(A, b);
+    const float two = __fmul_ru(2.0f, delta.tensor), inv = A.xinv[b];
     if (bad || (A.n1[b] == 0.0f && A.r1[b] == 0.0f && two < INFINITY)) {
       // no list, or that of a query of zeros (as padding is): every label's score is 0
       if (tid == 0) A.listed[b] = 0;
@@ -933,7 +955,7 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
                 A.near_l[(size_t)b * kMaxNear + at] = i;
               }
             } else if (at < kMaxBlocks) {
-              blocks[at] = i;
+              U.blocks[at] = i;
             }
           }
         });
@@ -946,13 +968,13 @@ __global__ void __launch_bounds__(kJoinThreads) label_join_kernel(const Args A) 
           A.fail[atomicAdd(&A.counts->nfail, 1)] = b;
         } else if (!keep) {
           at0 = atomicAdd(&A.counts->nitems, found);
-          A.from[b] = __fsub_rd(__fmul_rd(low, inv), two);
+          A.from[b] = __fsub_rd(__fmul_rd(low, inv), __fadd_ru(delta.tensor, delta.near));
         }
       }
       __syncthreads();
-      if (ok && keep) rank_near<kFormat, kJoinThreads>(A, b, xs, found, m, logs, &S, &R);
+      if (ok && keep) rank_near<kFormat, kJoinThreads>(A, b, xs, found, delta.tensor, m, logs, &S, &U.rank);
       else if (ok)
-        for (int i = tid; i < found; i += kJoinThreads) A.items[at0 + i] = make_int2(b, blocks[i]);
+        for (int i = tid; i < found; i += kJoinThreads) A.items[at0 + i] = make_int2(b, U.blocks[i]);
     }
   }
 
@@ -1018,12 +1040,13 @@ __global__ void __launch_bounds__(kNearThreads) label_rank_kernel(const Args A) 
   float* xs = reinterpret_cast<float*>(dyn);           // [d]
   __shared__ SmemB S;
   __shared__ SmemR R;
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x;
   load_query<kNearThreads>(A, b, xs);
   pdl_wait();
   pdl_trigger();
   if (A.listed[b] == 0) return;                        // answered, or a failed query already
-  rank_near<kFormat, kNearThreads>(A, b, xs, A.nnear[b], A.rowstat[2 * b], A.rowstat[2 * b + 1], &S, &R);
+  rank_near<kFormat, kNearThreads>(A, b, xs, A.nnear[b], deltas_of(A, b).near, A.rowstat[2 * b], A.rowstat[2 * b + 1],
+                                   &S, &R);
 }
 
 // ---------------------------------------------------------------- 4. exact path
@@ -1153,7 +1176,7 @@ __global__ void __launch_bounds__(kExactThreads) label_exact_kernel(const Args A
 // ---------------------------------------------------------------- host
 struct Layout {
   int G, nblk, nblkp, pairs, streams;
-  size_t xa, xb, xinv, n1, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
+  size_t xa, xb, xinv, n1, nw, r1, rflag, counts, fail, done, bmax, items, listed, nnear, near_v, near_l, from, part, sk, si,
       rowstat, total;
 };
 
@@ -1188,6 +1211,7 @@ Layout layout_of(const elmo_head* h, int32_t B, int32_t k) {
   o.xb = take(fp8 ? (size_t)B * h->d : 0);
   o.xinv = take(4 * (size_t)B);
   o.n1 = take(4 * (size_t)B);
+  o.nw = take(4 * (size_t)B);
   o.r1 = take(4 * (size_t)B);
   o.rflag = take(4 * (size_t)B);
   o.counts = take(sizeof(Counts));
@@ -1278,10 +1302,10 @@ cudaError_t launch_label_logprobs(elmo_head* h, const uint16_t* X, int32_t B, co
   A.nblk = o.nblk; A.nblkp = o.nblkp; A.pairs = o.pairs; A.streams = o.streams;
   A.fmt = w_format(h);
   A.segs = exact_segments(h->L, B, k);
-  const int nsteps = (fp8 ? 2 : 1) * ((h->d * (fp8 ? 1 : 2) + 127) / 128) * 4;
-  A.gamma = (float)nsteps * (fp8 ? 32.0f : 16.0f) * 0x1p-24f;
+  A.eps = 1.5f * (fp8 ? 32.0f : 16.0f) * 0x1p-25f;
   A.xinv = reinterpret_cast<float*>(ws + o.xinv);
   A.n1 = reinterpret_cast<float*>(ws + o.n1);
+  A.nw = reinterpret_cast<float*>(ws + o.nw);
   A.r1 = reinterpret_cast<float*>(ws + o.r1);
   A.rflag = reinterpret_cast<int32_t*>(ws + o.rflag);
   A.counts = reinterpret_cast<Counts*>(ws + o.counts);

@@ -199,6 +199,52 @@ def test_products_that_the_tensor_cores_cut_off(grid, L, d):
     h.close()
 
 
+@pytest.mark.parametrize("grid,L,d", [("bf16", 3000, 768), ("bf16", 20_000, 1024), ("e4m3", 20_000, 768), ("e5m2", 3000, 1024)])
+@pytest.mark.parametrize("place", [0, 16, 100, 384, 640, 700])
+def test_products_cut_off_from_the_large_one_on(grid, L, d, place):
+    """The same with the large product anywhere in the sum: what comes before it is not cut, and the bound, which counts
+    an element of the query for the instructions from its own on, still covers what comes after."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    rng = np.random.default_rng(d + place)
+    instructions = (d - place) // 16
+    big, x_small, w_small = 256.0, 1.75 * 2.0**-15, 0.140625
+    lift = 1.9 * instructions * 2.0**-21 * big
+    w = rng.normal(0, 0.02, (L, d))
+    a, b = L - 7, 40
+    w[a], w[b] = 0, 0
+    w[a, place:], w[b, place:] = w_small, -w_small
+    w[[a, b], place] = big
+    at = place + 1
+    w[a, at], w[b, at] = 0, np.float32(lift * 2.0**9)
+    x = np.full((2, d), x_small)
+    x[:, place], x[:, at] = 1, 2.0**-9
+    W, h = head_ops.head_of(elmo, w, grid)
+    X = head_ops.bf16(x)
+    z = X.double().cpu().numpy() @ W.double().cpu().numpy().T
+    order = np.argsort(-z, 1, kind="stable")[:, :2]             # a first, but for what the grid makes of the lift
+    assert set(order[0]) == {a, b}
+    one = head_ops.run(elmo, h, X, np.zeros(3, np.int32), np.zeros(0, np.int32), 1)[3]
+    assert (one == order[:, :1]).all()
+    h.close()
+
+
+@pytest.mark.parametrize("grid,L", [("e4m3", 100_003), ("bf16", 60_001), ("e5m2", 40_000)])
+def test_long_lists_of_the_widest_heads(grid, L):
+    """Many labels within the bound of the last listed one: 4096 weights a label, 64 best."""
+    need_gpu()
+    import precision_label_chunk_b200 as elmo
+    d, B, k = 4096, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(L)
+    W = (torch.randn(L, d, generator=g, device="cuda") * 0.02).to(head_ops.GRIDS[grid])
+    X = torch.randn(B, d, generator=g, device="cuda").to(torch.bfloat16)
+    h = elmo.elmo_init_head(W, grid)
+    idx = head_ops.run(elmo, h, X, np.zeros(B + 1, np.int32), np.zeros(0, np.int32), k)[3]
+    Z = torch.cat([X.double() @ W[a:a + 20_000].double().T for a in range(0, L, 20_000)], 1)
+    assert np.array_equal(idx, torch.topk(Z, k, 1)[1].int().cpu().numpy())
+    h.close()
+
+
 @pytest.mark.parametrize("grid", ["bf16", "e4m3", "e5m2"])
 def test_small_queries(grid):
     """Queries down to the smallest magnitudes beside ordinary ones: statistics and lists of each."""
