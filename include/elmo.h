@@ -512,7 +512,8 @@ typedef enum {
  *   top_idx_dev, top_logp_dev : int32 / fp32 [B x k], written: the labels with
  *                the largest scores, best first, ties to the lower label, and
  *                their log p; -1 and -inf beyond the labels that are neither
- *                masked nor NaN.  May be NULL with k = 0.
+ *                masked nor NaN.  May be NULL with k = 0.  Sorted rows and rows
+ *                with many equal scores take longer.
  *   work_dev, work_bytes : device memory of at least
  *                elmo_score_logprobs_workspace_bytes bytes, 16-byte aligned,
  *                of any content; calls that may overlap need their own.
@@ -576,9 +577,11 @@ elmo_status elmo_score_logprobs_backward(const void* Z_dev, elmo_score_dtype zt,
  * elmo_score_logprobs).  Scores of 2^127 and more, and sums that leave fp32's
  * range on the way to a score, make the log-sum-exp and the entropy infinite
  * or NaN; the list holds all the same.  Queries whose list the tensor-core
- * scores cannot settle (ties, sums that may leave fp32's range, weights that
- * are not finite) are ranked over all labels on the CUDA cores, which takes far
- * longer.  ELMO_EUNSUPPORTED on a head made by
+ * scores cannot settle are ranked over all labels on the CUDA cores, which
+ * takes far longer: many labels that tie with the k-th best or come close to it,
+ * one weight that stands far above all others (from some hundred times their
+ * deviation on: the scores' error bound goes with the largest weight), sums that
+ * may leave fp32's range, weights that are not finite.  ELMO_EUNSUPPORTED on a head made by
  * elmo_init_head_shard that does not hold all labels.
  * The workspace is the head's: the first call of a size allocates (call once
  * before capturing into a CUDA graph); calls on one head must not overlap on

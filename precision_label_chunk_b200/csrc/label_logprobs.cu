@@ -36,8 +36,8 @@
 //   4. queries with too many labels within 2 delta (ties), or with sums that
 //      may leave fp32's range, or a head that is not finite, rank all labels
 //      by exact scores on the CUDA cores: with all labels tied 0.35 ms for 500K
-//      bf16 labels x 768 and one query, 0.87 for 4; 21 ms for 3M E4M3 labels
-//      and 16.
+//      bf16 labels x 768 and one query, 0.87 for 4; 22 ms for 3M E4M3 labels
+//      and 16.  One weight far above all others does that too (see delta).
 //
 // delta = (eps nw + r1) max|W|, r1 the sum of what hi and lo leave.  How the
 // accumulating instructions round is documented nowhere.  Measured on B200, one
@@ -59,12 +59,15 @@
 // one of 4 takes 4 queries from 2.9 to 13 ms.
 //
 // Bounds and times on B200.  Few queries: the read of W; 500K bf16 labels x
-// 768, 4 queries: pass 126 us (6.1 TB/s), all of it 158.  Many: the MMAs, most
-// likely by the shared memory that they and the copies use with 64 labels an
-// instruction (tensor pipe 62 % busy, 500K labels); 3M E4M3 labels, 256 queries:
-// pass 1032 us, 2.3 PFLOP/s of 8-bit products (two a weight), all of it 1174 in
-// a loop, at the power limit and 1440 MHz; 1028 for single calls.  Narrow
-// heads: the epilogue; 1M labels x 64, 128 queries: 70 us.
+// 768, 4 queries: pass 123 us (6.2 TB/s), all of it 158.  Many: the tensor pipe is
+// the busiest unit (62 %, 500K E4M3 labels, 256 queries; issue slots 30, DRAM 29),
+// and what it waits for is not measured: most likely the shared memory that the
+// MMAs and the copies share, with 64 labels an instruction; 3M E4M3 labels, 256
+// queries: pass 1032 us, 2.3 PFLOP/s of 8-bit products (two a weight), all of it
+// 1175 in a loop, at the power limit and 1440 MHz; 1028 for single calls; 64 best
+// in place of 5 take 1305.  E5M2 1204.  500K bf16, 256 queries 285.  Small heads:
+// the launches; 20K bf16 labels x 256, 4 queries 31 us.  Narrow heads: the
+// epilogue; 1M labels x 64, 128 queries: 70 us.
 #include <cuda.h>
 #include <float.h>
 

@@ -42,10 +42,12 @@ using namespace tc;
 // step away from every midpoint.  Scales below 2^-100, whose own rounding may
 // be coarse, take the division.
 //
-// HBM-bound: the bytes of W, half a byte a weight, the scales.  A thread has
+// bf16 is HBM-bound: the bytes of W, half a byte a weight, the scales.  A thread has
 // kPackAt vectors in flight, each warp access contiguous (16 weights a thread,
 // two vectors apart, measured 214 us for 500K bf16 labels x 768).  On B200, for
-// those in groups of 64: 160 us to pack (6.1 TB/s), 156 us to unpack (6.3 TB/s).
+// those in groups of 64: 162 us to pack (6.0 TB/s), 160 us to unpack (6.1 TB/s).
+// 8-bit weights have half the bytes and more to do for each: E4M3 177 us (issue
+// slots 82 % busy, ALU 70, DRAM 36), E5M2 152.
 constexpr int kPackThreads = 256;
 constexpr int kPackAt = 4;
 
@@ -214,10 +216,11 @@ cudaError_t run_pack(const void* W, int64_t n8, int32_t group, uint32_t* codes, 
 // nothing of it lives on in the loop over the tiles: called from that loop it
 // cost registers, 124 us for 500K labels and 32 queries in place of 109.
 //
-// Bound by the read of the codes and the unpacking together (1M labels: DRAM
-// 56 %, issue slots 60 %): on B200, 3M labels x 768 in groups of 64 and one query
-// take 260 us in a loop (1.24 GB, 4.8 TB/s); the same ring with the arithmetic
-// left out takes 203 us.  500K labels, groups of 128, seven queries: 48 us.
+// Bound by no unit alone (1M labels, one query: issue slots 62 %, DRAM 57, ALU
+// 49; seven queries much the same): on B200, 3M labels x 768 in groups of 64 and
+// one query take 257 us in a loop (1.24 GB, 4.8 TB/s); the same ring with the
+// arithmetic left out takes 203.  500K labels, groups of 128, seven queries: 48
+// us; groups of 64, 32 queries: 107.
 // Eight warps of labels in place of sixteen took 307 us against 237; 24 warps,
 // larger requests and whole rows a stage changed nothing.
 constexpr int kQKB = 128;                 // bytes of a box's row: 256 codes
